@@ -12,6 +12,12 @@ streams into its calls.  PyTorch provides device memory and streams.
 M x N row-major; tensors are passed as raw storage (any torch dtype), their
 element type is ``dtype_ab`` / ``dtype_c``.  ``wgrad`` takes NHWC ``x`` and
 ``dy`` and writes the fp32 KRSC filter gradient ``dw``.
+
+Around the products of a layer: ``rmsnorm`` (with the residual's addition and
+the output as 16-bit values, e4m3 codes with row scales, or MX blocks) and
+``rmsnorm_bwd``; ``mx_quant`` / ``mx_dequant`` to and from MX blocks of e4m3 or
+e2m1 (4-bit) codes; and ``gemm(dtype_ab="e2m1", scale_mode="mx",
+tile="auto")`` for their product.
 """
 
 from . import _lib
@@ -19,7 +25,8 @@ from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  
                    skg_plan_wgrad, skg_profile_events, skg_run_gemm, skg_run_wgrad,
                    skg_tile_info, skg_gemm_workspace_bytes, skg_wgrad_workspace_bytes,
                    skg_fixup_timeouts, skg_run_wgrad_static, skg_plan_fwd, skg_plan_dgrad,
-                   skg_run_fwd, skg_run_dgrad, MODES, REDUCTIONS, DTYPES, TILES, SCALE_MODES,
+                   skg_run_fwd, skg_run_dgrad, skg_run_rmsnorm, skg_run_rmsnorm_bwd,
+                   skg_rmsnorm_bwd_workspace_bytes, skg_run_mx_quant, skg_run_mx_dequant, MODES, REDUCTIONS, DTYPES, TILES, SCALE_MODES,
                    SK_ORDERS)
 
 __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd", "plan_dgrad",
@@ -30,7 +37,10 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "skg_run_gemm", "skg_run_wgrad", "skg_tile_info", "skg_profile_events",
            "skg_gemm_workspace_bytes", "skg_wgrad_workspace_bytes", "skg_fixup_timeouts",
            "skg_run_wgrad_static", "skg_plan_fwd", "skg_plan_dgrad", "skg_run_fwd",
-           "skg_run_dgrad"]
+           "skg_run_dgrad", "rmsnorm", "rmsnorm_bwd", "mx_quant", "mx_dequant",
+           "rmsnorm_args", "rmsnorm_bwd_args", "mx_args", "skg_run_rmsnorm",
+           "skg_run_rmsnorm_bwd", "skg_rmsnorm_bwd_workspace_bytes", "skg_run_mx_quant",
+           "skg_run_mx_dequant"]
 
 
 def _enum(table, v, what):
@@ -58,7 +68,7 @@ def gemm_args(A=None, B=None, C=None, *, M, N, K, dtype_ab, dtype_c, lda=None, l
     a.ldb = K if ldb is None else ldb
     a.ldc = N if ldc is None else ldc
     a.scale_a, a.scale_b = _ptr(scale_a), _ptr(scale_b)
-    a.tile_id = _enum(TILES, tile, "tile")
+    a.tile_id = _lib.TILE_AUTO if tile == "auto" else _enum(TILES, tile, "tile")
     a.mode = _enum(MODES, mode, "mode")
     a.reduction = _enum(REDUCTIONS, reduction, "reduction")
     a.ctas = ctas
@@ -177,3 +187,88 @@ def dgrad(dy, filt, dx, workspace=None, stream=None, **kw):
     plan = skg_plan_dgrad(args).as_dict()
     _run(skg_run_dgrad, args, plan, dx.device, workspace, stream)
     return plan
+
+
+def rmsnorm_args(x=None, y=None, *, rows, cols, dtype, dtype_y=None, weight=None, dtype_w=None,
+                 residual=None, h=None, rstd=None, y_scale=None, scale_mode="rowcol", eps=1e-5,
+                 ldx=None, ldr=None, ldh=None, ldy=None):
+    a = _lib.skg_norm_args_t()
+    a.rows, a.cols = rows, cols
+    a.dtype = _enum(DTYPES, dtype, "dtype")
+    a.dtype_w = a.dtype if dtype_w is None else _enum(DTYPES, dtype_w, "dtype")
+    a.dtype_y = a.dtype if dtype_y is None else _enum(DTYPES, dtype_y, "dtype")
+    a.scale_mode = _enum(SCALE_MODES, scale_mode, "scale mode")
+    a.x, a.residual, a.weight, a.h = _ptr(x), _ptr(residual), _ptr(weight), _ptr(h)
+    a.y, a.y_scale, a.rstd = _ptr(y), _ptr(y_scale), _ptr(rstd)
+    a.ldx = cols if ldx is None else ldx
+    a.ldr = cols if ldr is None else ldr
+    a.ldh = cols if ldh is None else ldh
+    a.ldy = cols if ldy is None else ldy
+    a.eps = eps
+    return a
+
+
+def rmsnorm_bwd_args(dy=None, h=None, rstd=None, dx=None, *, rows, cols, dtype, weight=None,
+                     dtype_w=None, dres=None, dw=None, lddy=None, ldh=None, lddres=None,
+                     lddx=None):
+    a = _lib.skg_norm_bwd_args_t()
+    a.rows, a.cols = rows, cols
+    a.dtype = _enum(DTYPES, dtype, "dtype")
+    a.dtype_w = a.dtype if dtype_w is None else _enum(DTYPES, dtype_w, "dtype")
+    a.dy, a.h, a.rstd, a.weight = _ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight)
+    a.dres, a.dx, a.dw = _ptr(dres), _ptr(dx), _ptr(dw)
+    a.lddy = cols if lddy is None else lddy
+    a.ldh = cols if ldh is None else ldh
+    a.lddres = cols if lddres is None else lddres
+    a.lddx = cols if lddx is None else lddx
+    return a
+
+
+def mx_args(x=None, q=None, scales=None, *, rows, cols, dtype, dtype_q, kq=None, ldx=None,
+            ldq=None, transpose=False):
+    a = _lib.skg_mx_args_t()
+    a.rows, a.cols = rows, cols
+    if kq is None:
+        kq = ((rows if transpose else cols) + 31) // 32 * 32
+    a.kq = kq
+    a.dtype = _enum(DTYPES, dtype, "dtype")
+    a.dtype_q = _enum(DTYPES, dtype_q, "dtype")
+    a.x, a.q, a.scales = _ptr(x), _ptr(q), _ptr(scales)
+    a.ldx = cols if ldx is None else ldx
+    a.ldq = kq if ldq is None else ldq
+    a.transpose = 1 if transpose else 0
+    return a
+
+
+def rmsnorm(x, y, stream=None, **kw):
+    """Enqueue y = norm(x + residual) * weight on ``stream``; ``h`` receives
+    the sum, ``rstd`` the rows' factors for ``rmsnorm_bwd``, ``y_scale`` the
+    scales of a quantised output (``dtype_y``)."""
+    skg_run_rmsnorm(rmsnorm_args(x, y, **kw), _launch_stream(stream).cuda_stream)
+
+
+def rmsnorm_bwd(dy, h, rstd, dx, workspace=None, stream=None, **kw):
+    """Enqueue the norm's gradient on ``stream``: dx (plus ``dres``) and the
+    fp32 weight gradient ``dw``; either may be None."""
+    args = rmsnorm_bwd_args(dy, h, rstd, dx, **kw)
+    s = _launch_stream(stream)
+    ws = workspace
+    if ws is None and args.dw:
+        import torch
+        ws = torch.empty(max(skg_rmsnorm_bwd_workspace_bytes(args), 1), dtype=torch.uint8,
+                         device=kw["dw"].device)
+        ws.record_stream(s)
+    skg_run_rmsnorm_bwd(args, 0 if ws is None else ws.data_ptr(),
+                        0 if ws is None else ws.numel() * ws.element_size(), s.cuda_stream)
+
+
+def mx_quant(x, q, scales, stream=None, **kw):
+    """Enqueue the MX quantisation of ``x`` into codes ``q`` and E8M0
+    ``scales`` on ``stream``; ``transpose=True`` quantises along the columns and
+    writes the codes transposed."""
+    skg_run_mx_quant(mx_args(x, q, scales, **kw), _launch_stream(stream).cuda_stream)
+
+
+def mx_dequant(q, scales, x, stream=None, **kw):
+    """Enqueue x = the values of MX codes ``q`` with ``scales`` on ``stream``."""
+    skg_run_mx_dequant(mx_args(x, q, scales, **kw), _launch_stream(stream).cuda_stream)

@@ -11,20 +11,23 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libskgemm.so")
 
 SKG_OK, SKG_ERR_HIP, SKG_ERR_UNSUPPORTED = 0, -1, -2
-F16, BF16, F8E4M3, F32, F8E5M2 = 0, 1, 2, 3, 4
+F16, BF16, F8E4M3, F32, F8E5M2, F4E2M1 = 0, 1, 2, 3, 4, 5
 SCALE_ROWCOL, SCALE_TENSOR, SCALE_MX_E8M0 = 0, 1, 2
 MODE_DP, MODE_DP_SK, MODE_PERSISTENT, MODE_SPLITK, MODE_AUTO = 0, 1, 2, 3, 4
 RED_LINEAR, RED_TREE, RED_ATOMIC, RED_WORKSPACE, RED_AUTO, RED_SCATTER = 0, 1, 2, 3, 4, 5
 OP_GEMM, OP_WGRAD, OP_FWD, OP_DGRAD = 0, 1, 2, 3
+TILE_AUTO = -1
 TILE_128x128x32, TILE_256x256x64, TILE_256x256x128, TILE_32x64x64, TILE_128x128x64, \
-    TILE_256x128x64, TILE_128x128x128, TILE_64x144x32, TILE_128x64x32 = range(9)
-TILE_COUNT = 9
+    TILE_256x128x64, TILE_128x128x128, TILE_64x144x32, TILE_128x64x32, TILE_256x256x256, \
+    TILE_128x128x256 = range(11)
+TILE_COUNT = 11
 
 MODES = {"dp": MODE_DP, "dp_sk": MODE_DP_SK, "persistent": MODE_PERSISTENT,
          "splitk": MODE_SPLITK, "auto": MODE_AUTO}
 REDUCTIONS = {"linear": RED_LINEAR, "tree": RED_TREE, "atomic": RED_ATOMIC,
               "workspace": RED_WORKSPACE, "auto": RED_AUTO, "scatter": RED_SCATTER}
-DTYPES = {"f16": F16, "bf16": BF16, "e4m3": F8E4M3, "f32": F32, "e5m2": F8E5M2}
+DTYPES = {"f16": F16, "bf16": BF16, "e4m3": F8E4M3, "f32": F32, "e5m2": F8E5M2,
+          "e2m1": F4E2M1}
 SCALE_MODES = {"rowcol": SCALE_ROWCOL, "tensor": SCALE_TENSOR, "mx": SCALE_MX_E8M0}
 SK_ORDER_AUTO, SK_ORDER_BLOCK, SK_ORDER_XCD, SK_ORDER_KMAJOR = 0, 1, 2, 3
 SK_ORDERS = {"auto": SK_ORDER_AUTO, "block": SK_ORDER_BLOCK, "xcd": SK_ORDER_XCD,
@@ -33,7 +36,8 @@ TILES = {"128x128x32": TILE_128x128x32, "256x256x64": TILE_256x256x64,
          "256x256x128": TILE_256x256x128, "32x64x64": TILE_32x64x64,
          "128x128x64": TILE_128x128x64, "256x128x64": TILE_256x128x64,
          "128x128x128": TILE_128x128x128, "64x144x32": TILE_64x144x32,
-         "128x64x32": TILE_128x64x32}
+         "128x64x32": TILE_128x64x32, "256x256x256": TILE_256x256x256,
+         "128x128x256": TILE_128x128x256}
 
 
 class skg_tile_info_t(ctypes.Structure):
@@ -69,6 +73,38 @@ class skg_conv_args_t(ctypes.Structure):
                  "groups", "dtype", "dtype_out")] + \
                [("act", ctypes.c_void_p), ("filt", ctypes.c_void_p), ("out", ctypes.c_void_p)] + \
                [(n, ctypes.c_int32) for n in ("tile_id", "mode", "reduction", "ctas", "sk_order")]
+
+
+class skg_norm_args_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dtype_w", ctypes.c_int32),
+                ("dtype_y", ctypes.c_int32), ("scale_mode", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("weight", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("y_scale", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class skg_norm_bwd_args_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dtype_w", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dres", ctypes.c_void_p), ("lddres", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dw", ctypes.c_void_p)]
+
+
+class skg_mx_args_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kq", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dtype_q", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("transpose", ctypes.c_int32)]
 
 
 class skg_plan_t(ctypes.Structure):
@@ -112,7 +148,17 @@ EXPORTS = {
                                    ctypes.c_size_t, ctypes.c_void_p]),
     "skg_run_dgrad": (ctypes.c_int, [ctypes.POINTER(skg_conv_args_t), ctypes.c_void_p,
                                      ctypes.c_size_t, ctypes.c_void_p]),
+    "skg_run_rmsnorm": (ctypes.c_int, [ctypes.POINTER(skg_norm_args_t), ctypes.c_void_p]),
+    "skg_rmsnorm_bwd_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(skg_norm_bwd_args_t),
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "skg_run_rmsnorm_bwd": (ctypes.c_int, [ctypes.POINTER(skg_norm_bwd_args_t), ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p]),
+    "skg_run_mx_quant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
+    "skg_run_mx_dequant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
 }
+
+# Longest row of the norm and its gradient.
+NORM_MAX_COLS = 32768
 
 # Bytes of the library's own scratch array used by skg_run_wgrad_static.
 STATIC_SCRATCH_BYTES = 33 << 20
@@ -239,3 +285,25 @@ def skg_run_fwd(args, ws_ptr, ws_bytes, stream_ptr):
 
 def skg_run_dgrad(args, ws_ptr, ws_bytes, stream_ptr):
     return check(load().skg_run_dgrad(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))
+
+
+def skg_run_rmsnorm(args, stream_ptr):
+    return check(load().skg_run_rmsnorm(ctypes.byref(args), stream_ptr))
+
+
+def skg_rmsnorm_bwd_workspace_bytes(args):
+    out = ctypes.c_size_t()
+    check(load().skg_rmsnorm_bwd_workspace_bytes(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def skg_run_rmsnorm_bwd(args, ws_ptr, ws_bytes, stream_ptr):
+    return check(load().skg_run_rmsnorm_bwd(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))
+
+
+def skg_run_mx_quant(args, stream_ptr):
+    return check(load().skg_run_mx_quant(ctypes.byref(args), stream_ptr))
+
+
+def skg_run_mx_dequant(args, stream_ptr):
+    return check(load().skg_run_mx_dequant(ctypes.byref(args), stream_ptr))

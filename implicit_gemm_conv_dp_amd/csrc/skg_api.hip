@@ -63,7 +63,7 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   int occ = 0;
   hipError_t e;
   if (op == SKG_OP_GEMM) {
-    GemmInst in = gemm_instance(tile_id, dtype, SKG_SCALE_ROWCOL);
+    GemmInst in = gemm_instance(tile_id, dtype, dtype == SKG_F4E2M1 ? SKG_SCALE_MX_E8M0 : SKG_SCALE_ROWCOL);
     if (!in.occupancy) return unsupported("no GEMM instance for this tile and dtype");
     e = in.occupancy(&occ);
   } else if (op == SKG_OP_WGRAD) {
@@ -467,6 +467,15 @@ int run_conv(const skg_conv_args_t* a, bool dgrad, void* ws, size_t ws_bytes, hi
 }
 
 }  // namespace
+
+int check_device(int* cus) {
+  DeviceRec d;
+  const int rc = current_device(&d);
+  if (rc) return rc;
+  if (!d.gfx950) return unsupported("unsupported arch " + d.arch + " (the engine is built for gfx950)");
+  *cus = d.cus;
+  return SKG_OK;
+}
 }  // namespace skg
 
 using namespace skg;
@@ -499,9 +508,11 @@ int skg_profile_events(void* start, void* stop) {
   return SKG_OK;
 }
 
-int skg_plan_gemm(const skg_gemm_args_t* a, skg_plan_t* out) {
+int skg_plan_gemm(const skg_gemm_args_t* args, skg_plan_t* out) {
   try {
     clear_error();
+    if (!args) return unsupported("null arguments");
+    const skg_gemm_args_t resolved = resolve_gemm(args), *a = &resolved;
     int rc = validate_gemm(a);
     if (rc) return rc;
     if (!out) return unsupported("null output");
@@ -567,7 +578,8 @@ int skg_fixup_timeouts(uint32_t* count, int32_t reset) {
     if (!count) return unsupported("null output");
     hipError_t (*const units[])(uint32_t*, bool) = {wait_timeouts_gemm_f16, wait_timeouts_gemm_bf16,
                                                     wait_timeouts_gemm_f8,  wait_timeouts_wgrad,
-                                                    wait_timeouts_fwd,      wait_timeouts_dgrad};
+                                                    wait_timeouts_fwd,      wait_timeouts_dgrad,
+                                                    wait_timeouts_gemm_f4};
     uint32_t total = 0;
     for (auto fn : units) {
       uint32_t c = 0;
@@ -582,9 +594,11 @@ int skg_fixup_timeouts(uint32_t* count, int32_t reset) {
   }
 }
 
-int skg_run_gemm(const skg_gemm_args_t* a, void* ws, size_t ws_bytes, void* stream) {
+int skg_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream) {
   try {
     clear_error();
+    if (!args) return unsupported("null arguments");
+    const skg_gemm_args_t resolved = resolve_gemm(args), *a = &resolved;
     int rc = validate_gemm(a);
     if (rc) return rc;
     if (!a->A || !a->B || !a->C) return unsupported("null A, B or C");
@@ -607,8 +621,15 @@ int skg_run_gemm(const skg_gemm_args_t* a, void* ws, size_t ws_bytes, void* stre
     rc = check_run(pl, ws, ws_bytes, cus, per_cu);
     if (rc) return rc;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    rc = reset_scratch(pl, ws, st);
-    if (rc) return rc;
+    if (a->dtype_ab == SKG_F4E2M1 && pl.reduction != SKG_RED_ATOMIC) {
+      // Kernel resets, so that the call may be captured into a graph.
+      const size_t bytes = !pl.sk_ctas ? 0 : (size_t)(handoff_reduction(pl.reduction) ? pl.flags_bytes : pl.workspace_bytes);
+      hipError_t e = zero_fill(ws, bytes, st);
+      if (e != hipSuccess) return hip_failure(std::string("reset: ") + hipGetErrorString(e));
+    } else {
+      rc = reset_scratch(pl, ws, st);
+      if (rc) return rc;
+    }
     if (pl.reduction == SKG_RED_ATOMIC && pl.sk_ctas) {
       hipError_t e = hipMemset2DAsync(a->C, (size_t)a->ldc * 4, 0, (size_t)a->N * 4, (size_t)a->M, st);
       if (e != hipSuccess) return hip_failure(std::string("zeroing C: ") + hipGetErrorString(e));
@@ -620,8 +641,8 @@ int skg_run_gemm(const skg_gemm_args_t* a, void* ws, size_t ws_bytes, void* stre
     g.M = (int)a->M;
     g.N = (int)a->N;
     g.K = (int)a->K;
-    g.lda_b = (uint32_t)(a->lda * elem_bytes(a->dtype_ab));
-    g.ldb_b = (uint32_t)(a->ldb * elem_bytes(a->dtype_ab));
+    g.lda_b = (uint32_t)row_bytes(a->dtype_ab, a->lda);
+    g.ldb_b = (uint32_t)row_bytes(a->dtype_ab, a->ldb);
     g.ldc = (int)a->ldc;
     g.sa = a->scale_a;
     g.sb = a->scale_b;

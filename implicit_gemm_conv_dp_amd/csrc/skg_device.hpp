@@ -21,7 +21,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-enum { DT_F16 = 0, DT_BF16 = 1, DT_F8 = 2, DT_F32 = 3, DT_BF8 = 4 };
+enum { DT_F16 = 0, DT_BF16 = 1, DT_F8 = 2, DT_F32 = 3, DT_BF8 = 4, DT_F4 = 5 };
 enum { MODE_DP = 0, MODE_DP_SK = 1, MODE_PERSISTENT = 2 };
 enum { RED_LINEAR = 0, RED_TREE = 1, RED_ATOMIC = 2, RED_WORKSPACE = 3, RED_SCATTER = 5 };
 
@@ -258,10 +258,12 @@ struct MfmaF8x32 {
     c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FMT, FMT, 0, 0, 0, 0);
   }
   // With OCP MX block scales: each lane's operand data is one 32-element
-  // block along K (32 bytes), and the lane's E8M0 scale byte (bits 7:0 of
+  // block along K (32 bytes), and the lane's E8M0 scale byte (byte BYTE of
   // sa / sb) multiplies that block: 2^(code - 127).
+  template <int BYTE>
   SKG_DEV static void run_scaled(acc_t& c, const frag_t& a, const frag_t& b, uint32_t sa, uint32_t sb) {
-    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FMT, FMT, 0, (int)sa, 0, (int)sb);
+    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FMT, FMT, 0, (int)(sa >> (8 * BYTE) & 0xffu), 0,
+                                                        (int)(sb >> (8 * BYTE) & 0xffu));
   }
 };
 template <int FMT>
@@ -281,6 +283,25 @@ template <>
 struct Mfma<DT_BF8, 32> : MfmaF8x32<1> {};
 template <>
 struct Mfma<DT_BF8, 16> : MfmaF8x16<1> {};
+// fp4 (OCP E2M1, two codes a byte, the even K index in the low four bits):
+// format code 4 of the same family, at twice the fp8 rate.  A lane's operand
+// data is one 32-element block along K in 16 bytes (the upper half of the
+// instruction's eight operand registers is not read); lane l holds row
+// l % MN and block l / MN of the instruction's K extent, which the lane's
+// scale byte multiplies.  The byte is chosen by the instruction itself
+// (operand select), so a word of four scales needs no shifting.
+SKG_DEV i32x8 f4_operand(const i32x4& v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+template <>
+struct Mfma<DT_F4, 32> {
+  static constexpr int OPB = 16, KB = 32, NACC = 16;
+  typedef f32x16 acc_t;
+  typedef i32x4 frag_t;
+  template <int BYTE>
+  SKG_DEV static void run_scaled(acc_t& c, const frag_t& a, const frag_t& b, uint32_t sa, uint32_t sb) {
+    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f4_operand(a), f4_operand(b), c, 4, 4, BYTE, (int)sa, BYTE,
+                                                        (int)sb);
+  }
+};
 
 // One operand fragment from two 16-byte LDS reads (OPB = 32) or one.
 template <class FragT>

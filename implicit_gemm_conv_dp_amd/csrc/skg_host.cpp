@@ -23,6 +23,7 @@ thread_local std::string g_last_error;
 constexpr int M_F16 = 1 << SKG_F16;
 constexpr int M_BF16 = 1 << SKG_BF16;
 constexpr int M_F8 = 1 << SKG_F8E4M3 | 1 << SKG_F8E5M2;
+constexpr int M_F4 = 1 << SKG_F4E2M1;
 
 // Must agree with the kernel instances compiled in skg_api.hip.
 const TileDesc kTiles[SKG_TILE_COUNT] = {
@@ -35,6 +36,8 @@ const TileDesc kTiles[SKG_TILE_COUNT] = {
     /* 128x128x128 */ {128, 128, 128, 4, M_F8, 0, 0},
     /* 64x144x32   */ {64, 144, 32, 4, 0, M_F16 | M_BF16, 0, 4},
     /* 128x64x32   */ {128, 64, 32, 4, 0, 0, M_F16 | M_BF16, 4},
+    /* 256x256x256 */ {256, 256, 256, 4, M_F4, 0, 0},
+    /* 128x128x256 */ {128, 128, 256, 4, M_F4, 0, 0},
 };
 
 // Offsets inside one buffer are 32-bit on the device (buffer resources).
@@ -56,6 +59,8 @@ const TileDesc* tile_desc(int tile_id) {
   if (tile_id < 0 || tile_id >= SKG_TILE_COUNT) return nullptr;
   return &kTiles[tile_id];
 }
+
+int elem_bits(int dtype) { return dtype == SKG_F4E2M1 ? 4 : 8 * elem_bytes(dtype); }
 
 int elem_bytes(int dtype) {
   switch (dtype) {
@@ -313,22 +318,35 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
   return ceil_div(int64_t(a->k) * a->r * a->s * (a->c / a->groups) * 2, 256) * 256;
 }
 
+skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
+  skg_gemm_args_t r = *a;
+  if (r.tile_id != SKG_TILE_AUTO || r.dtype_ab != SKG_F4E2M1) return r;
+  r.tile_id = r.M > 1024 && r.N > 1024 ? SKG_TILE_256x256x256 : SKG_TILE_128x128x256;
+  return r;
+}
+
 int validate_gemm(const skg_gemm_args_t* a) {
   if (!a) return unsupported("null arguments");
   const TileDesc* t = tile_desc(a->tile_id);
   if (!t) return unsupported("unknown tile id");
   if (a->dtype_ab != SKG_F16 && a->dtype_ab != SKG_BF16 && a->dtype_ab != SKG_F8E4M3 &&
-      a->dtype_ab != SKG_F8E5M2)
+      a->dtype_ab != SKG_F8E5M2 && a->dtype_ab != SKG_F4E2M1)
     return unsupported("unsupported A/B dtype");
   if (a->scale_mode != SKG_SCALE_ROWCOL && a->scale_mode != SKG_SCALE_TENSOR &&
       a->scale_mode != SKG_SCALE_MX_E8M0)
     return unsupported("unknown scale mode");
   if (a->scale_mode == SKG_SCALE_MX_E8M0) {
-    if (a->dtype_ab != SKG_F8E4M3 && a->dtype_ab != SKG_F8E5M2)
-      return unsupported("MX block scales need fp8 or bf8 inputs");
-    if (a->tile_id != SKG_TILE_128x128x128 && a->tile_id != SKG_TILE_256x256x128)
-      return unsupported("MX block scales need the 128x128x128 or 256x256x128 tile");
+    if (a->dtype_ab == SKG_F4E2M1) {
+      if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need the 256x256x256 or 128x128x256 tile");
+    } else {
+      if (a->dtype_ab != SKG_F8E4M3 && a->dtype_ab != SKG_F8E5M2)
+        return unsupported("MX block scales need fp8, bf8 or fp4 inputs");
+      if (a->tile_id != SKG_TILE_128x128x128 && a->tile_id != SKG_TILE_256x256x128)
+        return unsupported("MX block scales need the 128x128x128 or 256x256x128 tile");
+    }
     if (a->K % 128) return unsupported("MX block scales need K to be a multiple of 128");
+  } else if (a->dtype_ab == SKG_F4E2M1) {
+    return unsupported("fp4 inputs need MX block scales");
   }
   if (a->sk_order < SKG_SK_ORDER_AUTO || a->sk_order > SKG_SK_ORDER_KMAJOR)
     return unsupported("unknown stream-K CTA order");
@@ -342,11 +360,12 @@ int validate_gemm(const skg_gemm_args_t* a) {
   if (a->M <= 0 || a->N <= 0 || a->K <= 0) return unsupported("M, N and K must be positive");
   if (a->M > INT32_MAX || a->N > INT32_MAX || a->K > INT32_MAX) return unsupported("dimension too large");
   if (a->lda < a->K || a->ldb < a->K || a->ldc < a->N) return unsupported("leading dimension too small");
-  const int eb = elem_bytes(a->dtype_ab), ec = elem_bytes(a->dtype_c);
-  if ((a->K * eb) % 16 || (a->lda * eb) % 16 || (a->ldb * eb) % 16)
+  const int bits = elem_bits(a->dtype_ab), ec = elem_bytes(a->dtype_c);
+  if (a->dtype_ab == SKG_F4E2M1 && a->ldc > INT32_MAX) return unsupported("leading dimension too large");
+  if ((a->K * bits) % 128 || (a->lda * bits) % 128 || (a->ldb * bits) % 128)
     return unsupported("K, lda and ldb must be multiples of 16 bytes");
   if ((a->ldc * ec) % 16) return unsupported("ldc must be a multiple of 16 bytes");
-  if (int64_t(t->tm) * a->lda * eb > kMaxBufferBytes || int64_t(t->tn) * a->ldb * eb > kMaxBufferBytes)
+  if (t->tm * row_bytes(a->dtype_ab, a->lda) > kMaxBufferBytes || t->tn * row_bytes(a->dtype_ab, a->ldb) > kMaxBufferBytes)
     return unsupported("row pitch too large for 32-bit tile offsets");
   return SKG_OK;
 }

@@ -18,6 +18,9 @@ int unsupported(const std::string& msg);
 // Returns -1 after recording msg.
 int hip_failure(const std::string& msg);
 
+// CU count of the current device; -1 without one, -2 if it is not gfx950.
+int check_device(int* cus);
+
 struct TileDesc {
   int tm, tn, tk, n_waves;
   int gemm_mask;   // 1 << skg_dtype accepted as GEMM A/B
@@ -43,6 +46,10 @@ inline bool whole_slices(const skg_plan_t& p) {
          p.sk_ctas == p.sk_tiles * (p.iters_per_tile / p.iters_per_sk_cta);
 }
 
+// Bits of one element, and bytes of n of them (n * bits a multiple of 8).
+int elem_bits(int dtype);
+inline int64_t row_bytes(int dtype, int64_t n) { return n * elem_bits(dtype) / 8; }
+// Bytes of one element (not for fp4).
 int elem_bytes(int dtype);
 
 // GEMM-shaped view of a problem: what the partitioner needs.
@@ -63,6 +70,8 @@ int resolve_sk_order(int requested, bool wgrad);
 
 // Argument checks that need no device (a0 of the hot path).
 int validate_gemm(const skg_gemm_args_t* a);
+// *a with SKG_TILE_AUTO resolved (fp4 only; other arguments unchanged).
+skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a);
 int validate_wgrad(const skg_wgrad_args_t* a);
 int validate_conv(const skg_conv_args_t* a, bool dgrad);
 

@@ -133,7 +133,7 @@ struct WgradParams {
 
 // ---------------------------------------------------------------------------
 // MX_: the operand slots also hold each row's E8M0 block scales of the
-// iteration (4 bytes per row after the row data).
+// iteration (one byte per 32 elements of K, after the row data).
 // BDG_ > 0: block-diagonal grouped tile holding BDG_ whole groups of 16
 // channels, one wave per group: along M for the wgrad (WgradBdLoader),
 // along N for the forward convolution and dgrad (ConvBdLoader); BDC_ of
@@ -143,9 +143,13 @@ template <int DT_, int TM_, int TN_, int TK_, int WM_, int WN_, int MN_, int RBS
 struct TileCfg {
   static constexpr int DT = DT_, TM = TM_, TN = TN_, TK = TK_, WM = WM_, WN = WN_, MN = MN_;
   static constexpr bool MX = MX_;
-  static constexpr int SCB = MX_ ? 4 : 0;  // scale bytes per row in a slot
-  static constexpr int ESZ = DT == DT_F8 || DT == DT_BF8 ? 1 : 2;
-  static constexpr int RB = TK * ESZ;  // LDS row bytes (K contiguous)
+  static constexpr int SCB = MX_ ? TK / 32 : 0;  // scale bytes per row in a slot
+  static constexpr int SCW = (SCB + 3) / 4;      // the same in words of four scales
+  static constexpr int EBITS = DT == DT_F4 ? 4 : DT == DT_F8 || DT == DT_BF8 ? 8 : 16;
+  static constexpr int ESZ = EBITS / 8;  // 0: two elements a byte
+  // Bytes of n elements (fp4: n is a multiple of 32).
+  SKG_DEV static int kbytes(int n) { return EBITS >= 8 ? n * ESZ : n / 2; }
+  static constexpr int RB = TK * EBITS / 8;  // LDS row bytes (K contiguous)
   static constexpr int CPR = RB / 16;  // 16-byte chunks per row
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int WTM = TM / WM, WTN = TN / WN;
@@ -237,7 +241,7 @@ struct GemmLoader {
     rb = make_rsrc(g.B + (size_t)n0 * g.ldb_b, (uint32_t)min((int64_t)rows_b * g.ldb_b, (int64_t)0x7fffffff));
     lda_b = g.lda_b;
     ldb_b = g.ldb_b;
-    kbytes = (uint32_t)g.K * Cfg::ESZ;
+    kbytes = (uint32_t)Cfg::kbytes(g.K);
     row0 = tid / Cfg::CPR;
     cb = (uint32_t)(tid % Cfg::CPR) * 16;
   }
@@ -306,7 +310,7 @@ struct DmaRows {
     stepb = STEP * g.ldb_b;
     // Clamped at zero: with K shorter than one LDS row the chunk may start
     // past K, and a wrapped limit would let it read the row's padding.
-    lim = (uint32_t)max(g.K * Cfg::ESZ - chunk * 16, 0);
+    lim = (uint32_t)max(Cfg::kbytes(g.K) - chunk * 16, 0);
   }
 
   // RBX bytes of K starting at byte kb of every row, A rows into `la`, B
@@ -392,35 +396,41 @@ struct GemmGrpLoader : DmaRows<Cfg, Cfg::RB> {
   SKG_DEV void finish_refill(Refill&) const {}
 };
 
-// GEMM with OCP MX block scales (fp8 / bf8, K a multiple of the tile's K):
-// each group also carries the E8M0 scale words of its rows for the MAC
-// iteration (4 bytes = the 4 blocks of 32 K elements a 128-byte row holds,
-// at row*(K/32) + it*4 of the row-major M x K/32 or N x K/32 scale array),
-// one 4-byte direct-to-LDS instruction per wave placed after the slot's row
-// data, so the engine's waits and barriers order them with the tile.
+// GEMM with OCP MX block scales (K a multiple of 128): each group also
+// carries the E8M0 scale words of its rows for the MAC iteration (SCW words
+// of four blocks of 32 K elements, one word for the 128 fp8 / bf8 elements a
+// 128-byte row holds and two for its 256 fp4 elements, at row*(K/32) +
+// it*4*SCW of the row-major M x K/32 or N x K/32 scale array), one 4-byte
+// direct-to-LDS instruction per wave and word placed after the slot's row
+// data (word w of row r at (w*rows + r)*4), so the engine's waits and barriers
+// order them with the tile.  A word past K (the second of an fp4 tail) is not
+// read but zero filled: it scales zero codes, and 2^-127 keeps them zero where
+// a neighbouring row's NaN scale would not.
 template <class Cfg>
 struct MxGrpLoader : GemmGrpLoader<Cfg> {
   typedef GemmGrpLoader<Cfg> Base;
   typedef DmaRows<Cfg, Cfg::RB> Rows;
   static constexpr bool kMx = true;
-  static_assert(Cfg::MX && Cfg::RB == 128 && Cfg::TK == 128, "MX: 4 scale blocks per 128-byte row");
+  static constexpr int W = Cfg::SCW;
+  static_assert(Cfg::MX && Cfg::RB == 128 && Cfg::SCB == 4 * W, "MX: whole words of scales per 128-byte row");
   static_assert(Cfg::TM % 64 == 0 && Cfg::TN % 64 == 0 && (Cfg::TM / 64) <= Cfg::NW &&
                     Cfg::NW % (Cfg::TM / 64) == 0 && Cfg::NW % (Cfg::TN / 64) == 0,
                 "one 64-row scale chunk per wave");
-  // DMA instructions per group and thread: the rows plus one scale word.
-  static constexpr int UA = Rows::UA + 1, UB = Rows::UB + 1;
+  // DMA instructions per group and thread: the rows plus the scale words.
+  static constexpr int UA = Rows::UA + W, UB = Rows::UB + W;
 
   __amdgpu_buffer_rsrc_t rsa, rsb;
+  uint32_t kb32;        // scale bytes per row
   uint32_t sofa, sofb;  // this lane's scale-row byte offset (row * K/32)
   int cha, chb;         // 64-row chunk of the tile this wave's scale DMA fills
 
   SKG_DEV void init(const GemmParams& g, int m0, int n0, int tid) {
     Base::init(g, m0, n0, tid);
-    const uint32_t kb32 = (uint32_t)g.K / 32;
+    kb32 = (uint32_t)g.K / 32;
     const char* sa = (const char*)g.sa;
     const char* sb = (const char*)g.sb;
-    rsa = make_rsrc(sa + (size_t)m0 * kb32, (uint32_t)(g.M - m0) * kb32);
-    rsb = make_rsrc(sb + (size_t)n0 * kb32, (uint32_t)(g.N - n0) * kb32);
+    rsa = make_rsrc(sa + (size_t)m0 * kb32, (uint32_t)min((int64_t)(g.M - m0) * kb32, (int64_t)0x7fffffff));
+    rsb = make_rsrc(sb + (size_t)n0 * kb32, (uint32_t)min((int64_t)(g.N - n0) * kb32, (int64_t)0x7fffffff));
     const int lane = tid & 63;
     cha = this->wave % (Cfg::TM / 64);
     chb = this->wave % (Cfg::TN / 64);
@@ -428,34 +438,41 @@ struct MxGrpLoader : GemmGrpLoader<Cfg> {
     sofb = (uint32_t)(chb * 64 + lane) * kb32;
   }
 
-  SKG_DEV void scales_a(int it, SKG_LDS char* slot, bool live) const {
-    dma4(rsa, lds_addr(slot + Cfg::TM * Cfg::RB + cha * 256), live ? sofa + (uint32_t)it * 4 : kOOB);
+  SKG_DEV void scale_a(int it, SKG_LDS char* slot, bool live, int w) const {
+    const uint32_t o = (uint32_t)(it * W + w) * 4;
+    dma4(rsa, lds_addr(slot + Cfg::TM * (Cfg::RB + 4 * w) + cha * 256),
+         live && (W == 1 || o < kb32) ? sofa + o : kOOB);
   }
-  SKG_DEV void scales_b(int it, SKG_LDS char* slot, bool live) const {
-    dma4(rsb, lds_addr(slot + Cfg::TN * Cfg::RB + chb * 256), live ? sofb + (uint32_t)it * 4 : kOOB);
+  SKG_DEV void scale_b(int it, SKG_LDS char* slot, bool live, int w) const {
+    const uint32_t o = (uint32_t)(it * W + w) * 4;
+    dma4(rsb, lds_addr(slot + Cfg::TN * (Cfg::RB + 4 * w) + chb * 256),
+         live && (W == 1 || o < kb32) ? sofb + o : kOOB);
   }
 
   SKG_DEV void issue_live(int j, int it, SKG_LDS char* slot, bool live) const {
     Base::issue_live(j, it, slot, live);
-    if ((j & 1) == 0)
-      scales_a(it, slot, live);
-    else
-      scales_b(it, slot, live);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if ((j & 1) == 0)
+        scale_a(it, slot, live, w);
+      else
+        scale_b(it, slot, live, w);
+    }
   }
   SKG_DEV void issue(int j, int it, SKG_LDS char* slot) const { issue_live(j, it, slot, true); }
 
   // DMA instruction N of a refill spread among the MFMAs, in the order of
-  // issue_live: the B group's rows, its scale word, then the A group's.
+  // issue_live: the B group's rows, its scale words, then the A group's.
   template <int N>
   SKG_DEV void refill(const typename Base::Refill& r) const {
     if constexpr (N < Rows::UB)
       Base::template refill<N>(r);
-    else if constexpr (N == Rows::UB)
-      scales_b(r.it_b, r.slot_b, r.live_b);
+    else if constexpr (N < UB)
+      scale_b(r.it_b, r.slot_b, r.live_b, N - Rows::UB);
     else if constexpr (N < UB + Rows::UA)
       Base::template refill<Rows::UB + (N - UB)>(r);
     else
-      scales_a(r.it_a, r.slot_a, r.live_a);
+      scale_a(r.it_a, r.slot_a, r.live_a, N - UB - Rows::UA);
   }
 };
 
@@ -1072,15 +1089,16 @@ struct Engine {
   SKG_LDS char* lds;
   int tid, lane, wave, wm, wn;
   acc_t acc[Cfg::FM][Cfg::FN];
-  // MX: this iteration's and the next one's scale words per fragment, each
-  // already shifted so that byte 0 is the lane's block of k-step 0 and
-  // byte 2 that of k-step 1.
+  // MX: this iteration's and the next one's scale words per fragment (word
+  // w: k-steps 2w and 2w+1), each already shifted so that byte 0 is the
+  // lane's block of the even k-step and byte 2 that of the odd one.
   static constexpr bool kMx = LoaderMx<Loader>::value;
   // One CTA per CU: the burst schedule spreads its refills among the MFMAs
   // (grp_iter_burst).
   static constexpr bool kDefer = Cfg::MIN_CTAS == 1;
   static constexpr bool kBd = Cfg::BDG > 0;  // block-diagonal grouped wgrad tile
-  uint32_t msa[Cfg::FM], msb[Cfg::FN], nsa[Cfg::FM], nsb[Cfg::FN];
+  static constexpr int SCW = Cfg::SCW > 0 ? Cfg::SCW : 1;
+  uint32_t msa[Cfg::FM][SCW], msb[Cfg::FN][SCW], nsa[Cfg::FM][SCW], nsb[Cfg::FN][SCW];
 
   SKG_DEV Engine(const Params& prm_, const KPlan& p_, const Scratch& s_, SKG_LDS char* lds_)
       : prm(prm_), p(p_), s(s_), lds(lds_) {
@@ -1141,9 +1159,12 @@ struct Engine {
   // One MFMA of block (f, g); the B fragment goes first (transposed block),
   // and with MX its scale is the instruction's first scale operand.
   SKG_DEV void mfma(int f, int g, const Frag& a, const Frag& b, int ks) {
-    if constexpr (kMx)
-      Cfg::Op::run_scaled(acc[f][g], b, a, (msb[g] >> (16 * ks)) & 0xffu, (msa[f] >> (16 * ks)) & 0xffu);
-    else
+    if constexpr (kMx) {
+      if (ks & 1)
+        Cfg::Op::template run_scaled<2>(acc[f][g], b, a, msb[g][ks >> 1], msa[f][ks >> 1]);
+      else
+        Cfg::Op::template run_scaled<0>(acc[f][g], b, a, msb[g][ks >> 1], msa[f][ks >> 1]);
+    } else
       Cfg::Op::run(acc[f][g], b, a);
   }
 
@@ -1156,19 +1177,24 @@ struct Engine {
   }
 
   // MX: the scale words of the iteration in slots sa (A) and sb (B): the
-  // word of the lane's row (A) or column (B), shifted right by 8 bits in
+  // words of the lane's row (A) or column (B), shifted right by 8 bits in
   // the upper half of the wave, whose operand data is the second block of
   // each k-step.
-  SKG_DEV void read_scales(uint32_t (&ra)[Cfg::FM], uint32_t (&rb)[Cfg::FN], const SKG_LDS char* sa,
-                           const SKG_LDS char* sb) const {
+  SKG_DEV void read_scales(uint32_t (&ra)[Cfg::FM][SCW], uint32_t (&rb)[Cfg::FN][SCW],
+                           const SKG_LDS char* sa, const SKG_LDS char* sb) const {
     if constexpr (kMx) {
       const int r = lane % Cfg::MN, sh = 8 * (lane / Cfg::MN);
 #pragma unroll
-      for (int f = 0; f < Cfg::FM; ++f)
-        ra[f] = *(const SKG_LDS uint32_t*)(sa + Cfg::TM * Cfg::RB + (wm * Cfg::WTM + f * Cfg::MN + r) * 4) >> sh;
+      for (int w = 0; w < SCW; ++w) {
 #pragma unroll
-      for (int g = 0; g < Cfg::FN; ++g)
-        rb[g] = *(const SKG_LDS uint32_t*)(sb + Cfg::TN * Cfg::RB + (wn * Cfg::WTN + g * Cfg::MN + r) * 4) >> sh;
+        for (int f = 0; f < Cfg::FM; ++f)
+          ra[f][w] = *(const SKG_LDS uint32_t*)(sa + Cfg::TM * (Cfg::RB + 4 * w) +
+                                                (wm * Cfg::WTM + f * Cfg::MN + r) * 4) >> sh;
+#pragma unroll
+        for (int g = 0; g < Cfg::FN; ++g)
+          rb[g][w] = *(const SKG_LDS uint32_t*)(sb + Cfg::TN * (Cfg::RB + 4 * w) +
+                                                (wn * Cfg::WTN + g * Cfg::MN + r) * 4) >> sh;
+      }
     }
   }
 
@@ -1622,9 +1648,12 @@ struct Engine {
     mma_rows(fa[CB], fb[CB], Cfg::FM / 2, Cfg::FM, KL);
     if constexpr (kMx && !LAST) {
 #pragma unroll
-      for (int f = 0; f < Cfg::FM; ++f) msa[f] = nsa[f];
+      for (int w = 0; w < SCW; ++w) {
 #pragma unroll
-      for (int g = 0; g < Cfg::FN; ++g) msb[g] = nsb[g];
+        for (int f = 0; f < Cfg::FM; ++f) msa[f][w] = nsa[f][w];
+#pragma unroll
+        for (int g = 0; g < Cfg::FN; ++g) msb[g][w] = nsb[g][w];
+      }
     }
   }
 

@@ -32,6 +32,7 @@ GemmInst gemm_instance(int tile_id, int dtype, int scale_mode);
 GemmInst gemm_instance_f16(int tile_id, bool tensor_scales);
 GemmInst gemm_instance_bf16(int tile_id, bool tensor_scales);
 GemmInst gemm_instance_f8(int tile_id, int dtype, int scale_mode);
+GemmInst gemm_instance_f4(int tile_id);
 WgradInst wgrad_instance(int tile_id, int dtype);
 ConvInst fwd_instance(int tile_id, int dtype);
 ConvInst dgrad_instance(int tile_id, int dtype);
@@ -41,6 +42,7 @@ ConvInst dgrad_instance(int tile_id, int dtype);
 hipError_t wait_timeouts_gemm_f16(uint32_t* out, bool reset);
 hipError_t wait_timeouts_gemm_bf16(uint32_t* out, bool reset);
 hipError_t wait_timeouts_gemm_f8(uint32_t* out, bool reset);
+hipError_t wait_timeouts_gemm_f4(uint32_t* out, bool reset);
 hipError_t wait_timeouts_wgrad(uint32_t* out, bool reset);
 hipError_t wait_timeouts_fwd(uint32_t* out, bool reset);
 hipError_t wait_timeouts_dgrad(uint32_t* out, bool reset);

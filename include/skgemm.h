@@ -4,8 +4,9 @@
  * One library, libskgemm.so, serves two workloads with one tiled MFMA
  * engine:
  *   - GEMM in the "rcr" layout (row-major A, column-major B, row-major C) on
- *     fp16, bf16 or OCP fp8 e4m3 inputs with optional per-row A and
- *     per-column B fp32 scales, fp32 accumulation;
+ *     fp16, bf16, OCP fp8 or OCP fp4 inputs with optional per-row A and
+ *     per-column B fp32 scales (fp8) or MX block scales (fp8, fp4), fp32
+ *     accumulation;
  *   - backward-weight convolution (wgrad) of NHWC activations as an implicit
  *     GEMM whose M is the output channels (conv groups folded into M per
  *     group), N the filter taps times input channels of a group, and whose
@@ -59,10 +60,14 @@ enum skg_dtype {
   SKG_BF16 = 1,    /* bfloat16 */
   SKG_F8E4M3 = 2,  /* OCP fp8 E4M3 (bias 7, max 448, no inf), the gfx950 fp8 */
   SKG_F32 = 3,     /* IEEE binary32 (outputs only) */
-  SKG_F8E5M2 = 4   /* OCP bf8 E5M2 (bias 15, max 57344, inf and NaN: the upper
+  SKG_F8E5M2 = 4,  /* OCP bf8 E5M2 (bias 15, max 57344, inf and NaN: the upper
                       byte of an IEEE binary16), the gfx950 bf8 ("gemm_rowcolquant
                       dispatcher bridge" PR: fp8/bf8 rcr scope; OCP encoding on
                       gfx950 per its round-3 fixes) */
+  SKG_F4E2M1 = 5   /* OCP fp4 E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+                      negatives, sign in bit 3), two codes a byte, the even
+                      element in the low four bits; GEMM inputs with MX block
+                      scales, and what the MX quantiser writes */
 };
 
 /* How scale_a / scale_b apply.  Row/column scaling is the "gemm_rowcolquant
@@ -86,10 +91,11 @@ enum skg_scale_mode {
    *                    2^(code-127), 255 = NaN) for one block of 32
    *                    consecutive K elements of a row of A or a column of B:
    *                    C[m][n] = round(sum_b 2^(sa[m][b]-127) 2^(sb[n][b]-127)
-   *                    sum_{k in b} a(m,k) b(k,n)).  fp8 / bf8 inputs, the
-   *                    128x128x128 or 256x256x128 tile, K a multiple of 128,
-   *                    both pointers non-NULL and 16-byte aligned; no
-   *                    further scale. */
+   *                    sum_{k in b} a(m,k) b(k,n)).  fp8 / bf8 inputs with
+   *                    the 128x128x128 or 256x256x128 tile, or fp4 inputs
+   *                    with a 256-deep one; K a multiple of 128, both
+   *                    pointers non-NULL and 16-byte aligned; no further
+   *                    scale. */
   SKG_SCALE_MX_E8M0 = 2
 };
 
@@ -199,6 +205,9 @@ enum skg_sk_order {
 /* Compiled tile instances.  TM x TN x TK in elements; each instance exists
  * for the operations and input types skg_tile_info reports. */
 enum skg_tile {
+  /* fp4 GEMM only: the call picks the tile from M, N and K (the plan's tm, tn
+     and tk report it). */
+  SKG_TILE_AUTO = -1,
   SKG_TILE_128x128x32 = 0,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x256x64 = 1,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x256x128 = 2,  /* fp8 GEMM (also with MX block scales), 4 waves */
@@ -215,7 +224,9 @@ enum skg_tile {
                                 of 16 input and 16 output channels (GEMM-N =
                                 64 channels), two filter taps per MAC
                                 iteration, 4 waves */
-  SKG_TILE_COUNT = 9
+  SKG_TILE_256x256x256 = 9,  /* fp4 GEMM with MX block scales, 4 waves */
+  SKG_TILE_128x128x256 = 10, /* fp4 GEMM with MX block scales, 4 waves */
+  SKG_TILE_COUNT = 11
 };
 
 enum skg_op { SKG_OP_GEMM = 0, SKG_OP_WGRAD = 1, SKG_OP_FWD = 2, SKG_OP_DGRAD = 3 };
@@ -246,7 +257,7 @@ typedef struct skg_tile_info {
  * columns of C keep what they held. */
 typedef struct skg_gemm_args {
   int64_t M, N, K;
-  int32_t dtype_ab;        /* SKG_F16, SKG_BF16, SKG_F8E4M3 or SKG_F8E5M2 */
+  int32_t dtype_ab;        /* SKG_F16, SKG_BF16, SKG_F8E4M3, SKG_F8E5M2 or SKG_F4E2M1 */
   int32_t dtype_c;         /* SKG_F16, SKG_BF16 or SKG_F32 */
   const void* A;
   int64_t lda;
@@ -454,6 +465,103 @@ int skg_run_wgrad_static(const skg_wgrad_args_t* args, void* stream);
  * their flags and a spin limit of 64 polls, so every hand-off wait gives up
  * quickly and the kernel still ends. */
 int skg_fixup_timeouts(uint32_t* count, int32_t reset);
+
+/* --- Low-precision layer operators --------------------------------------------
+ * What a layer needs around the products: the norm that feeds them, with its
+ * output already in their 8- or 4-bit operand form, the norm's gradient, and
+ * quantisation to and from MX blocks.  Status codes, ownership and streams as
+ * above.  Pointers need only their elements' alignment; rows of 16-byte
+ * aligned pointers and pitches are the fastest.  Zero rows are accepted and
+ * write nothing (the norm's gradient: dw = 0).  Nothing here synchronises,
+ * allocates or uses a memset, so every call may be captured into a graph. */
+
+/* Longest row of the norm and its gradient. */
+#define SKG_NORM_MAX_COLS 32768
+
+/* Root-mean-square norm with the residual's addition.  Per row:
+ *   h = round(x + residual)       in the rows' type (h = x without residual);
+ *   s = 1 / sqrt(mean(h^2) + eps) fp32 (stored in rstd for the gradient);
+ *   y = h * s * weight            (weight 1 when NULL).
+ * y is written
+ *   - in the rows' type (dtype_y == dtype), rounded once;
+ *   - as e4m3 codes of y / d with one fp32 scale d = max(max|y| / 448, 2^-126)
+ *     a row (SKG_F8E4M3 with SKG_SCALE_ROWCOL: y and y_scale are A and scale_a
+ *     of skg_run_gemm).  A NaN or infinity in a row gives it a scale of NaN;
+ *   - as MX blocks (SKG_F8E4M3 or SKG_F4E2M1 with SKG_SCALE_MX_E8M0; cols a
+ *     multiple of 32, y_scale rows x cols/32 E8M0 codes), as skg_run_mx_quant
+ *     makes them from the fp32 y. */
+typedef struct skg_norm_args {
+  int64_t rows, cols;
+  int32_t dtype;           /* x, residual, h: SKG_F16, SKG_BF16 or SKG_F32 */
+  int32_t dtype_w;         /* weight: dtype or SKG_F32 */
+  int32_t dtype_y;         /* dtype, SKG_F8E4M3 or SKG_F4E2M1 */
+  int32_t scale_mode;      /* of a quantised y: SKG_SCALE_ROWCOL or SKG_SCALE_MX_E8M0 */
+  const void* x;
+  int64_t ldx;             /* row pitches in elements */
+  const void* residual;    /* or NULL */
+  int64_t ldr;
+  const void* weight;      /* cols values, or NULL */
+  void* h;                 /* or NULL: not stored; may be x or residual */
+  int64_t ldh;
+  void* y;
+  int64_t ldy;
+  void* y_scale;           /* of a quantised y */
+  float* rstd;             /* rows floats, or NULL */
+  float eps;
+} skg_norm_args_t;
+
+/* Gradient of the norm.  With g = dy * weight:
+ *   dx = s * (g - h s^2 mean(g h)) + dres   (the gradient of x and of the
+ *        residual alike; dres, or NULL, is what reaches h from above);
+ *   dw = sum over rows of dy * h * s        fp32, in a fixed order.
+ * A quantised y passes its gradient through unchanged.  dx (which may be dy
+ * or dres) or dw may be NULL.  The workspace holds partial sums of dw. */
+typedef struct skg_norm_bwd_args {
+  int64_t rows, cols;
+  int32_t dtype;           /* dy, h, dres, dx */
+  int32_t dtype_w;         /* weight: dtype or SKG_F32 */
+  const void* dy;
+  int64_t lddy;
+  const void* h;
+  int64_t ldh;
+  const float* rstd;
+  const void* weight;
+  const void* dres;
+  int64_t lddres;
+  void* dx;
+  int64_t lddx;
+  float* dw;
+} skg_norm_bwd_args_t;
+
+/* MX quantisation.  Blocks are 32 consecutive elements along the row, or with
+ * transpose along the column, in which case q is written transposed (cols
+ * rows of kq codes: the operand of a product that reduces over x's rows).
+ * Per block, E the exponent field of the largest magnitude as fp32: the
+ * scale code is max(E - emax, 0), emax 2 for e2m1 and 8 for e4m3, and the
+ * elements are x / 2^(code - 127) rounded to nearest even, saturating.  A
+ * block that holds an infinity or NaN gets code 255 and zero elements.
+ * kq (a multiple of 32) codes are written per line; those past x's end are
+ * zero, so a ragged reduction can be padded to what the product takes.
+ * skg_run_mx_dequant writes code * 2^(scale - 127), rounded to dtype, into x
+ * (rows x cols). */
+typedef struct skg_mx_args {
+  int64_t rows, cols;      /* of x */
+  int64_t kq;              /* codes along the quantised axis */
+  int32_t dtype;           /* x: SKG_F16, SKG_BF16 or SKG_F32 */
+  int32_t dtype_q;         /* SKG_F4E2M1 or SKG_F8E4M3 */
+  void* x;                 /* quant: read only */
+  int64_t ldx;             /* elements */
+  void* q;
+  int64_t ldq;             /* elements */
+  void* scales;            /* lines x kq/32 E8M0 codes */
+  int32_t transpose;
+} skg_mx_args_t;
+
+int skg_run_rmsnorm(const skg_norm_args_t* args, void* stream);
+int skg_rmsnorm_bwd_workspace_bytes(const skg_norm_bwd_args_t* args, size_t* out);
+int skg_run_rmsnorm_bwd(const skg_norm_bwd_args_t* args, void* ws, size_t ws_bytes, void* stream);
+int skg_run_mx_quant(const skg_mx_args_t* args, void* stream);
+int skg_run_mx_dequant(const skg_mx_args_t* args, void* stream);
 
 /* Timing hook for measurement: while set on the calling thread, every run
  * call records `start` (a hipEvent_t) on its stream immediately before the
