@@ -6,6 +6,7 @@ library is missing, loading it raises.
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libskgemm.so")
@@ -19,8 +20,9 @@ OP_GEMM, OP_WGRAD, OP_FWD, OP_DGRAD = 0, 1, 2, 3
 TILE_AUTO = -1
 TILE_128x128x32, TILE_256x256x64, TILE_256x256x128, TILE_32x64x64, TILE_128x128x64, \
     TILE_256x128x64, TILE_128x128x128, TILE_64x144x32, TILE_128x64x32, TILE_256x256x256, \
-    TILE_128x128x256 = range(11)
-TILE_COUNT = 11
+    TILE_128x128x256, TILE_16x16x512, TILE_16x32x512, \
+    TILE_16x64x512, TILE_32x32x512, TILE_32x64x512, TILE_48x32x512, TILE_64x64x512 = range(18)
+TILE_COUNT = 18
 
 MODES = {"dp": MODE_DP, "dp_sk": MODE_DP_SK, "persistent": MODE_PERSISTENT,
          "splitk": MODE_SPLITK, "auto": MODE_AUTO}
@@ -37,7 +39,10 @@ TILES = {"128x128x32": TILE_128x128x32, "256x256x64": TILE_256x256x64,
          "128x128x64": TILE_128x128x64, "256x128x64": TILE_256x128x64,
          "128x128x128": TILE_128x128x128, "64x144x32": TILE_64x144x32,
          "128x64x32": TILE_128x64x32, "256x256x256": TILE_256x256x256,
-         "128x128x256": TILE_128x128x256}
+         "128x128x256": TILE_128x128x256, "16x16x512": TILE_16x16x512, "16x32x512": TILE_16x32x512,
+         "16x64x512": TILE_16x64x512, "32x32x512": TILE_32x32x512,
+         "32x64x512": TILE_32x64x512, "48x32x512": TILE_48x32x512,
+         "64x64x512": TILE_64x64x512}
 
 
 class skg_tile_info_t(ctypes.Structure):
@@ -118,7 +123,14 @@ class skg_plan_t(ctypes.Structure):
                [("aux_bytes", ctypes.c_int64)]
 
     def as_dict(self):
-        return {n: getattr(self, n) for n, _ in self._fields_}
+        return dict(zip(_PLAN_NAMES, _PLAN_STRUCT.unpack(self)))
+
+
+# skg_plan_t as the struct module reads it (native alignment).
+_PLAN_NAMES = [n for n, _ in skg_plan_t._fields_]
+_PLAN_STRUCT = struct.Struct("@" + "".join("i" if t is ctypes.c_int32 else "q"
+                                           for _, t in skg_plan_t._fields_))
+assert _PLAN_STRUCT.size == ctypes.sizeof(skg_plan_t)
 
 
 EXPORTS = {

@@ -60,6 +60,21 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   int rc = current_device(&d);
   if (rc) return rc;
   if (!d.gfx950) return unsupported("unsupported arch " + d.arch + " (the engine is built for gfx950)");
+  // The runtime's answer for an instance does not change: asked for once.
+  struct Known {
+    int op, tile, dtype, occ;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    for (const Known& k : known)
+      if (k.op == op && k.tile == tile_id && k.dtype == dtype) {
+        *cus = d.cus;
+        *per_cu = k.occ;
+        return SKG_OK;
+      }
+  }
   int occ = 0;
   hipError_t e;
   if (op == SKG_OP_GEMM) {
@@ -79,6 +94,10 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   }
   if (e != hipSuccess) return hip_failure(std::string("occupancy query: ") + hipGetErrorString(e));
   if (occ <= 0) return unsupported("kernel instance cannot be resident on this device");
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    known.push_back({op, tile_id, dtype, occ});
+  }
   *cus = d.cus;
   *per_cu = occ;
   return SKG_OK;
@@ -106,7 +125,7 @@ int injected_fault() {
 
 FastDiv make_fastdiv(uint32_t d);
 
-KPlan to_kplan(const skg_plan_t& pl, int inject) {
+KPlan to_kplan(const skg_plan_t& pl, int inject, int cus) {
   KPlan k;
   k.tiles_m = (int)pl.tiles_m;
   k.tiles_n = (int)pl.tiles_n;
@@ -127,6 +146,7 @@ KPlan to_kplan(const skg_plan_t& pl, int inject) {
   k.fault = inject == INJECT_HANDOFF ? FAULT_NO_PUBLISH : FAULT_NONE;
   const int tn = k.tiles_n > 0 ? k.tiles_n : 1;
   k.dp_rows = k.dp_tiles / tn;
+  k.cus = cus;
   k.div_tiles_n = make_fastdiv((uint32_t)tn);
   k.div_groups = make_fastdiv((uint32_t)(kDpGroupRows * tn));
   return k;
@@ -307,7 +327,7 @@ int run_wgrad(const skg_wgrad_args_t* a, void* ws, size_t ws_bytes, hipStream_t 
   }
   const int inject = injected_fault();
   if (inject == INJECT_LAUNCH) return hip_failure("launch: failure injected by SKG_FAULT=launch");
-  hipError_t e = inst.launch(w, to_kplan(pl, inject), carve(pl, ws), st, g_ev_start, g_ev_stop);
+  hipError_t e = inst.launch(w, to_kplan(pl, inject, cus), carve(pl, ws), st, g_ev_start, g_ev_stop);
   if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   return SKG_OK;
 }
@@ -461,7 +481,7 @@ int run_conv(const skg_conv_args_t* a, bool dgrad, void* ws, size_t ws_bytes, hi
   }
   const int inject = injected_fault();
   if (inject == INJECT_LAUNCH) return hip_failure("launch: failure injected by SKG_FAULT=launch");
-  hipError_t e = inst.launch(c, to_kplan(pl, inject), carve(pl, ws), st, g_ev_start, g_ev_stop);
+  hipError_t e = inst.launch(c, to_kplan(pl, inject, cus), carve(pl, ws), st, g_ev_start, g_ev_stop);
   if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   return SKG_OK;
 }
@@ -649,7 +669,7 @@ int skg_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* s
     g.dtype_c = a->dtype_c == SKG_F32 ? DT_F32 : (a->dtype_c == SKG_F16 ? DT_F16 : DT_BF16);
     const int inject = injected_fault();
     if (inject == INJECT_LAUNCH) return hip_failure("launch: failure injected by SKG_FAULT=launch");
-    hipError_t e = inst.launch(g, to_kplan(pl, inject), carve(pl, ws), st, g_ev_start, g_ev_stop);
+    hipError_t e = inst.launch(g, to_kplan(pl, inject, cus), carve(pl, ws), st, g_ev_start, g_ev_stop);
     if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
     return SKG_OK;
   } catch (const std::exception& ex) {

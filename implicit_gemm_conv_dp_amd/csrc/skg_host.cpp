@@ -38,6 +38,13 @@ const TileDesc kTiles[SKG_TILE_COUNT] = {
     /* 128x64x32   */ {128, 64, 32, 4, 0, 0, M_F16 | M_BF16, 4},
     /* 256x256x256 */ {256, 256, 256, 4, M_F4, 0, 0},
     /* 128x128x256 */ {128, 128, 256, 4, M_F4, 0, 0},
+    /* 16x16x512 */ {16, 16, 512, 4, M_F4, 0, 0, 0, true},
+    /* 16x32x512 */ {16, 32, 512, 4, M_F4, 0, 0, 0, true},
+    /* 16x64x512 */ {16, 64, 512, 4, M_F4, 0, 0, 0, true},
+    /* 32x32x512 */ {32, 32, 512, 4, M_F4, 0, 0, 0, true},
+    /* 32x64x512 */ {32, 64, 512, 4, M_F4, 0, 0, 0, true},
+    /* 48x32x512 */ {48, 32, 512, 4, M_F4, 0, 0, 0, true},
+    /* 64x64x512 */ {64, 64, 512, 4, M_F4, 0, 0, 0, true},
 };
 
 // Offsets inside one buffer are 32-bit on the device (buffer resources).
@@ -147,6 +154,11 @@ int plan_launch(const GemmShape& g, const TileDesc& t, int mode, int reduction, 
                 int sk_order, int num_cus, int resident_per_cu, skg_plan_t* out) {
   const int requested = mode;
   int slices = 1;
+  if (t.direct && mode != SKG_MODE_AUTO && mode != SKG_MODE_DP)
+    return unsupported("this tile splits K within its workgroup: mode dp or auto");
+  // fp4: the dp kernels are ahead of every split over the whole sweep of
+  // resolve_gemm (1500x1500x4096 15.9 us against 30.3 on stream-K).
+  if ((t.gemm_mask & M_F4) && mode == SKG_MODE_AUTO) mode = SKG_MODE_DP;
   int rc = resolve_launch(g, mode, reduction, ctas, num_cus, resident_per_cu, slices);
   if (rc) return rc;
   rc = make_plan(g, t, mode, reduction, ctas, num_cus, resident_per_cu, out);
@@ -318,10 +330,40 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
   return ceil_div(int64_t(a->k) * a->r * a->s * (a->c / a->groups) * 2, 256) * 256;
 }
 
+// The fp4 tile of a call that leaves it open: the least of the times that these
+// models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
+// 8192, K 512 to 8192) on all tiles, each within 15 % or so of the measured.
+// - A direct tile's workgroups read their operands' rows at 30 kB/us a CU,
+//   whatever its shape: 1x8192x8192 8.3 us on 16x16 (12.7 on 16x64),
+//   48x4863x4096 8.3 on 16x64 (11.3 on 16x16), 1024x1024x1024 6.3 on 64x64
+//   (9.5 on 16x32).
+// - A ring tile costs a start and end and its iterations, a workgroup a CU at
+//   a time: 256x8192x8192 21.4 us on 128x128 (43.0 on direct 64x64, 48.4 on
+//   256x256), 4096x4096x1024 22.2 on 256x256 (25.9 on 128x128).
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   skg_gemm_args_t r = *a;
   if (r.tile_id != SKG_TILE_AUTO || r.dtype_ab != SKG_F4E2M1) return r;
-  r.tile_id = r.M > 1024 && r.N > 1024 ? SKG_TILE_256x256x256 : SKG_TILE_128x128x256;
+  r.tile_id = SKG_TILE_128x128x256;  // until a better one is found; also for sizes that are refused
+  if (r.M <= 0 || r.N <= 0 || r.K <= 0) return r;
+  const bool dp = r.mode == SKG_MODE_AUTO || r.mode == SKG_MODE_DP;
+  double best = 1e300;
+  for (int id = 0; id < SKG_TILE_COUNT; ++id) {
+    const TileDesc& t = kTiles[id];
+    if (!(t.gemm_mask & M_F4) || (t.direct && !dp)) continue;
+    const double rounds = (double)ceil_div(ceil_div(r.M, t.tm) * ceil_div(r.N, t.tn), 256);  // CUs of a gfx950
+    double us;
+    if (t.direct) {
+      const int64_t rows = std::min<int64_t>(t.tm, r.M) + std::min<int64_t>(t.tn, r.N);
+      us = 2.2 + rounds * (double)rows * (double)r.K * (0.5 + 1.0 / 32) / 30e3;
+    } else {
+      const double iters = (double)ceil_div(r.K, t.tk);
+      us = rounds * (t.tm == 256 ? 12 + 1.5 * iters : 5 + 0.45 * iters);
+    }
+    if (us < best) {
+      best = us;
+      r.tile_id = id;
+    }
+  }
   return r;
 }
 
@@ -337,7 +379,7 @@ int validate_gemm(const skg_gemm_args_t* a) {
     return unsupported("unknown scale mode");
   if (a->scale_mode == SKG_SCALE_MX_E8M0) {
     if (a->dtype_ab == SKG_F4E2M1) {
-      if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need the 256x256x256 or 128x128x256 tile");
+      if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need the 256x256x256, 128x128x256 or a 512-deep tile");
     } else {
       if (a->dtype_ab != SKG_F8E4M3 && a->dtype_ab != SKG_F8E5M2)
         return unsupported("MX block scales need fp8, bf8 or fp4 inputs");

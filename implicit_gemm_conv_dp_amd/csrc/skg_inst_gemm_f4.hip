@@ -1,20 +1,38 @@
 // fp4 (OCP E2M1) GEMM kernel instances with OCP MX block scales: 256x256x256
 // and 128x128x256 tiles (128-byte rows, like the 128-deep fp8 tiles).
+#include "skg_f4_direct.hpp"
+#include "skg_f4_tile.hpp"
 #include "skg_inst_gemm_common.hpp"
 
 namespace skg {
 namespace {
-template <int TM, int TN>
+template <int TM, int TN, int D>
 GemmInst f4_tile() {
   typedef TileCfg<DT_F4, TM, TN, 256, 2, 2, 32, 128, true> Cfg;
-  return {&launch_instance<Cfg, GemmMxProblem<Cfg>>, &occupancy_instance<Cfg, GemmMxProblem<Cfg>>};
+  return {[](const GemmParams& g, const KPlan& p, const Scratch& s, hipStream_t st, hipEvent_t ev0, hipEvent_t ev1) {
+            if (p.mode != MODE_DP) return launch_instance<Cfg, GemmMxProblem<Cfg>>(g, p, s, st, ev0, ev1);
+            hipError_t e;
+            if (ev0 && (e = hipEventRecord(ev0, st)) != hipSuccess) return e;
+            if ((e = f4_tile_launch<F4Tile<TM, TN, D>>(g, p, st)) != hipSuccess) return e;
+            return ev1 ? hipEventRecord(ev1, st) : hipSuccess;
+          },
+          &occupancy_instance<Cfg, GemmMxProblem<Cfg>>};
 }
 }  // namespace
 
 GemmInst gemm_instance_f4(int tile_id) {
-  if (tile_id == SKG_TILE_256x256x256) return f4_tile<256, 256>();
-  if (tile_id == SKG_TILE_128x128x256) return f4_tile<128, 128>();
-  return {nullptr, nullptr};
+  switch (tile_id) {
+    case SKG_TILE_256x256x256: return f4_tile<256, 256, 2>();
+    case SKG_TILE_128x128x256: return f4_tile<128, 128, 4>();
+    case SKG_TILE_16x16x512: return f4_direct<1, 1>();
+    case SKG_TILE_16x32x512: return f4_direct<1, 2>();
+    case SKG_TILE_16x64x512: return f4_direct<1, 4>();
+    case SKG_TILE_32x32x512: return f4_direct<2, 2>();
+    case SKG_TILE_32x64x512: return f4_direct<2, 4>();
+    case SKG_TILE_48x32x512: return f4_direct<3, 2>();
+    case SKG_TILE_64x64x512: return f4_direct<4, 4>();
+    default: return {nullptr, nullptr};
+  }
 }
 hipError_t wait_timeouts_gemm_f4(uint32_t* out, bool reset) { return unit_wait_timeouts(out, reset); }
 }  // namespace skg

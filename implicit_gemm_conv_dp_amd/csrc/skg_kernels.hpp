@@ -48,6 +48,7 @@ struct KPlan {
   int dp_rows;          // dp_tiles / tiles_n
   FastDiv div_tiles_n;  // by tiles_n
   FastDiv div_groups;   // by kDpGroupRows * tiles_n
+  int cus;              // compute units of the device
   // Row of the tile grid that tile id `tile` lies in.
   SKG_DEV int tile_row(int tile) const { return (int)fdiv((uint32_t)tile, div_tiles_n); }
 };

@@ -226,7 +226,17 @@ enum skg_tile {
                                 iteration, 4 waves */
   SKG_TILE_256x256x256 = 9,  /* fp4 GEMM with MX block scales, 4 waves */
   SKG_TILE_128x128x256 = 10, /* fp4 GEMM with MX block scales, 4 waves */
-  SKG_TILE_COUNT = 11
+  /* fp4 GEMM with MX block scales, 4 waves that split the reduction (512
+     elements of K among them) and read their operands straight into
+     registers; mode dp or auto, no workspace */
+  SKG_TILE_16x16x512 = 11,
+  SKG_TILE_16x32x512 = 12,
+  SKG_TILE_16x64x512 = 13,
+  SKG_TILE_32x32x512 = 14,
+  SKG_TILE_32x64x512 = 15,
+  SKG_TILE_48x32x512 = 16,
+  SKG_TILE_64x64x512 = 17,
+  SKG_TILE_COUNT = 18
 };
 
 enum skg_op { SKG_OP_GEMM = 0, SKG_OP_WGRAD = 1, SKG_OP_FWD = 2, SKG_OP_DGRAD = 3 };
