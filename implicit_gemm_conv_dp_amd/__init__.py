@@ -44,12 +44,12 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
 
 
 def _enum(table, v, what):
-    if isinstance(v, int):
-        return v
-    try:
-        return table[v]
-    except KeyError:
-        raise ValueError("unknown %s %r" % (what, v)) from None
+    r = table.get(v)
+    if r is None:
+        if isinstance(v, int):
+            return v
+        raise ValueError("unknown %s %r" % (what, v))
+    return r
 
 
 def _ptr(t):
@@ -59,22 +59,16 @@ def _ptr(t):
 def gemm_args(A=None, B=None, C=None, *, M, N, K, dtype_ab, dtype_c, lda=None, ldb=None,
               ldc=None, scale_a=None, scale_b=None, scale_mode="rowcol", tile, mode, reduction,
               ctas, sk_order="auto"):
-    a = _lib.skg_gemm_args_t()
-    a.M, a.N, a.K = M, N, K
-    a.dtype_ab = _enum(DTYPES, dtype_ab, "dtype")
-    a.dtype_c = _enum(DTYPES, dtype_c, "dtype")
-    a.A, a.B, a.C = _ptr(A), _ptr(B), _ptr(C)
-    a.lda = K if lda is None else lda
-    a.ldb = K if ldb is None else ldb
-    a.ldc = N if ldc is None else ldc
-    a.scale_a, a.scale_b = _ptr(scale_a), _ptr(scale_b)
-    a.tile_id = _lib.TILE_AUTO if tile == "auto" else _enum(TILES, tile, "tile")
-    a.mode = _enum(MODES, mode, "mode")
-    a.reduction = _enum(REDUCTIONS, reduction, "reduction")
-    a.ctas = ctas
-    a.scale_mode = _enum(SCALE_MODES, scale_mode, "scale mode")
-    a.sk_order = _enum(SK_ORDERS, sk_order, "stream-K order")
-    return a
+    # Positional, in the struct's order: a call for a few tokens spends more
+    # time here than on the GPU.
+    return _lib.skg_gemm_args_t(
+        M, N, K, _enum(DTYPES, dtype_ab, "dtype"), _enum(DTYPES, dtype_c, "dtype"),
+        _ptr(A), K if lda is None else lda, _ptr(B), K if ldb is None else ldb,
+        _ptr(C), N if ldc is None else ldc, _ptr(scale_a), _ptr(scale_b),
+        _lib.TILE_AUTO if tile == "auto" else _enum(TILES, tile, "tile"),
+        _enum(MODES, mode, "mode"), _enum(REDUCTIONS, reduction, "reduction"), ctas,
+        _enum(SCALE_MODES, scale_mode, "scale mode"),
+        _enum(SK_ORDERS, sk_order, "stream-K order"))
 
 
 def wgrad_args(x=None, dy=None, dw=None, *, n, h, w, c, k, r, s, stride=(1, 1), pad=(0, 0),
@@ -141,17 +135,43 @@ def _launch_stream(stream):
     return torch.cuda.current_stream() if stream is None else stream
 
 
+_current_handle = None
+
+
+def _handle(stream):
+    """The launch stream's handle.  Without a caller's stream that of torch's
+    current one, asked for without making a Stream object where torch offers it
+    (0.2 us against 2.9)."""
+    global _current_handle
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_handle is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw and device:
+            _current_handle = lambda: raw(device())
+        else:
+            _current_handle = lambda: torch.cuda.current_stream().cuda_stream
+    return _current_handle()
+
+
 def _run(run, args, plan, device, workspace, stream):
     """One run call.  A workspace the call allocates itself is handed to the
     caching allocator as used by the launch stream (record_stream), so its
     memory is not given to another allocation before the kernel is done
-    with it, whichever stream the caller passed."""
-    s = _launch_stream(stream)
-    ws = workspace
-    if ws is None:
+    with it, whichever stream the caller passed.  A plan without one allocates
+    nothing."""
+    if workspace is not None:
+        run(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _handle(stream))
+    elif not plan["workspace_bytes"]:
+        run(args, 0, 0, _handle(stream))
+    else:
+        s = _launch_stream(stream)
         ws = workspace_for(plan, device)
         ws.record_stream(s)
-    run(args, ws.data_ptr(), ws.numel() * ws.element_size(), s.cuda_stream)
+        run(args, ws.data_ptr(), ws.numel() * ws.element_size(), s.cuda_stream)
 
 
 def gemm(A, B, C, scale_a=None, scale_b=None, workspace=None, stream=None, **kw):
@@ -192,83 +212,68 @@ def dgrad(dy, filt, dx, workspace=None, stream=None, **kw):
 def rmsnorm_args(x=None, y=None, *, rows, cols, dtype, dtype_y=None, weight=None, dtype_w=None,
                  residual=None, h=None, rstd=None, y_scale=None, scale_mode="rowcol", eps=1e-5,
                  ldx=None, ldr=None, ldh=None, ldy=None):
-    a = _lib.skg_norm_args_t()
-    a.rows, a.cols = rows, cols
-    a.dtype = _enum(DTYPES, dtype, "dtype")
-    a.dtype_w = a.dtype if dtype_w is None else _enum(DTYPES, dtype_w, "dtype")
-    a.dtype_y = a.dtype if dtype_y is None else _enum(DTYPES, dtype_y, "dtype")
-    a.scale_mode = _enum(SCALE_MODES, scale_mode, "scale mode")
-    a.x, a.residual, a.weight, a.h = _ptr(x), _ptr(residual), _ptr(weight), _ptr(h)
-    a.y, a.y_scale, a.rstd = _ptr(y), _ptr(y_scale), _ptr(rstd)
-    a.ldx = cols if ldx is None else ldx
-    a.ldr = cols if ldr is None else ldr
-    a.ldh = cols if ldh is None else ldh
-    a.ldy = cols if ldy is None else ldy
-    a.eps = eps
-    return a
+    dt = _enum(DTYPES, dtype, "dtype")
+    return _lib.skg_norm_args_t(
+        rows, cols, dt, dt if dtype_w is None else _enum(DTYPES, dtype_w, "dtype"),
+        dt if dtype_y is None else _enum(DTYPES, dtype_y, "dtype"),
+        _enum(SCALE_MODES, scale_mode, "scale mode"), _ptr(x), cols if ldx is None else ldx,
+        _ptr(residual), cols if ldr is None else ldr, _ptr(weight), _ptr(h),
+        cols if ldh is None else ldh, _ptr(y), cols if ldy is None else ldy, _ptr(y_scale),
+        _ptr(rstd), eps)
 
 
 def rmsnorm_bwd_args(dy=None, h=None, rstd=None, dx=None, *, rows, cols, dtype, weight=None,
                      dtype_w=None, dres=None, dw=None, lddy=None, ldh=None, lddres=None,
                      lddx=None):
-    a = _lib.skg_norm_bwd_args_t()
-    a.rows, a.cols = rows, cols
-    a.dtype = _enum(DTYPES, dtype, "dtype")
-    a.dtype_w = a.dtype if dtype_w is None else _enum(DTYPES, dtype_w, "dtype")
-    a.dy, a.h, a.rstd, a.weight = _ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight)
-    a.dres, a.dx, a.dw = _ptr(dres), _ptr(dx), _ptr(dw)
-    a.lddy = cols if lddy is None else lddy
-    a.ldh = cols if ldh is None else ldh
-    a.lddres = cols if lddres is None else lddres
-    a.lddx = cols if lddx is None else lddx
-    return a
+    dt = _enum(DTYPES, dtype, "dtype")
+    return _lib.skg_norm_bwd_args_t(
+        rows, cols, dt, dt if dtype_w is None else _enum(DTYPES, dtype_w, "dtype"),
+        _ptr(dy), cols if lddy is None else lddy, _ptr(h), cols if ldh is None else ldh,
+        _ptr(rstd), _ptr(weight), _ptr(dres), cols if lddres is None else lddres, _ptr(dx),
+        cols if lddx is None else lddx, _ptr(dw))
 
 
 def mx_args(x=None, q=None, scales=None, *, rows, cols, dtype, dtype_q, kq=None, ldx=None,
             ldq=None, transpose=False):
-    a = _lib.skg_mx_args_t()
-    a.rows, a.cols = rows, cols
     if kq is None:
         kq = ((rows if transpose else cols) + 31) // 32 * 32
-    a.kq = kq
-    a.dtype = _enum(DTYPES, dtype, "dtype")
-    a.dtype_q = _enum(DTYPES, dtype_q, "dtype")
-    a.x, a.q, a.scales = _ptr(x), _ptr(q), _ptr(scales)
-    a.ldx = cols if ldx is None else ldx
-    a.ldq = kq if ldq is None else ldq
-    a.transpose = 1 if transpose else 0
-    return a
+    return _lib.skg_mx_args_t(
+        rows, cols, kq, _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, dtype_q, "dtype"), _ptr(x),
+        cols if ldx is None else ldx, _ptr(q), kq if ldq is None else ldq, _ptr(scales),
+        1 if transpose else 0)
 
 
 def rmsnorm(x, y, stream=None, **kw):
     """Enqueue y = norm(x + residual) * weight on ``stream``; ``h`` receives
     the sum, ``rstd`` the rows' factors for ``rmsnorm_bwd``, ``y_scale`` the
     scales of a quantised output (``dtype_y``)."""
-    skg_run_rmsnorm(rmsnorm_args(x, y, **kw), _launch_stream(stream).cuda_stream)
+    skg_run_rmsnorm(rmsnorm_args(x, y, **kw), _handle(stream))
 
 
 def rmsnorm_bwd(dy, h, rstd, dx, workspace=None, stream=None, **kw):
     """Enqueue the norm's gradient on ``stream``: dx (plus ``dres``) and the
     fp32 weight gradient ``dw``; either may be None."""
     args = rmsnorm_bwd_args(dy, h, rstd, dx, **kw)
-    s = _launch_stream(stream)
-    ws = workspace
-    if ws is None and args.dw:
-        import torch
-        ws = torch.empty(max(skg_rmsnorm_bwd_workspace_bytes(args), 1), dtype=torch.uint8,
-                         device=kw["dw"].device)
-        ws.record_stream(s)
-    skg_run_rmsnorm_bwd(args, 0 if ws is None else ws.data_ptr(),
-                        0 if ws is None else ws.numel() * ws.element_size(), s.cuda_stream)
+    ws, need = workspace, 0
+    if ws is not None:
+        need = ws.numel() * ws.element_size()
+    elif args.dw:
+        need = skg_rmsnorm_bwd_workspace_bytes(args)
+        if need:
+            import torch
+            ws = torch.empty(need, dtype=torch.uint8, device=kw["dw"].device)
+            if stream is not None:
+                ws.record_stream(stream)
+    skg_run_rmsnorm_bwd(args, _ptr(ws), need, _handle(stream))
 
 
 def mx_quant(x, q, scales, stream=None, **kw):
     """Enqueue the MX quantisation of ``x`` into codes ``q`` and E8M0
     ``scales`` on ``stream``; ``transpose=True`` quantises along the columns and
     writes the codes transposed."""
-    skg_run_mx_quant(mx_args(x, q, scales, **kw), _launch_stream(stream).cuda_stream)
+    skg_run_mx_quant(mx_args(x, q, scales, **kw), _handle(stream))
 
 
 def mx_dequant(q, scales, x, stream=None, **kw):
     """Enqueue x = the values of MX codes ``q`` with ``scales`` on ``stream``."""
-    skg_run_mx_dequant(mx_args(x, q, scales, **kw), _launch_stream(stream).cuda_stream)
+    skg_run_mx_dequant(mx_args(x, q, scales, **kw), _handle(stream))
