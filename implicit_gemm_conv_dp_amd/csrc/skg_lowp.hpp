@@ -67,6 +67,52 @@ SKG_DEV void store_chunk(typename Elem<DT>::raw* p, int n, const Chunk<DT>& c) {
   }
 }
 
+// Elements e0 .. e0+7 of a row of cols elements in two steps, so that a row's
+// loads are issued together, without a branch: the load takes the last
+// eight elements instead where these reach past the end, and place_chunk
+// then moves what is wanted into place and zeroes the rest.
+// TAIL: 0 where cols is a multiple of eight, 1 where it is not, 2 where it is
+// less than eight.
+template <int DT, int TAIL>
+SKG_DEV Chunk<DT> load_within(const typename Elem<DT>::raw* row, int e0, int cols) {
+  if constexpr (TAIL < 2) {
+    return reinterpret_cast<const Loose<Chunk<DT>>*>(row + min(e0, cols - 8))->c;
+  } else {
+    Chunk<DT> c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c.v[i] = row[min(i, cols - 1)];
+    return c;
+  }
+}
+template <int DT, int TAIL>
+SKG_DEV void place_chunk(Chunk<DT>& c, int e0, int cols) {
+  constexpr int W = sizeof(c) / 4, E = 8 / W;  // words, elements in each
+  struct Words {
+    uint32_t w[W];
+  };
+  Words u = __builtin_bit_cast(Words, c);
+  if (TAIL && e0 < cols && e0 + 8 > cols) {
+    const int d = TAIL == 1 ? e0 - (cols - 8) : 0, n = cols - e0;
+#pragma unroll
+    for (int b = 4; b >= E; b >>= 1)
+#pragma unroll
+      for (int i = 0; i < W; ++i) u.w[i] = d & b ? (i + b / E < W ? u.w[i + b / E] : 0) : u.w[i];
+    if constexpr (E == 2) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        u.w[i] = d & 1 ? u.w[i] >> 16 | (i + 1 < W ? u.w[i + 1] << 16 : 0) : u.w[i];
+        u.w[i] = 2 * i + 1 < n ? u.w[i] : 2 * i < n ? u.w[i] & 0xffffu : 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) u.w[i] = i < n ? u.w[i] : 0;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) u.w[i] = e0 < cols ? u.w[i] : 0;
+  c = __builtin_bit_cast(Chunk<DT>, u);
+}
+
 // --- reductions --------------------------------------------------------------
 struct OpSum {
   typedef float T;
@@ -107,11 +153,25 @@ SKG_DEV typename Op::T wave_reduce(typename Op::T v) {
   v = dpp_step<Op, 0x143, 0xc>(v);  // lane 31 onto the upper half
   return __builtin_bit_cast(typename Op::T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
-// Over WAVES waves; `slot` is WAVES words of LDS that nobody else uses until
-// the next workgroup barrier.
-template <class Op, int WAVES>
+// Over a group of LANES neighbouring lanes (8 .. 64); every lane has the
+// result.
+template <class Op, int LANES>
+SKG_DEV typename Op::T lanes_reduce(typename Op::T v) {
+  if constexpr (LANES == 64) {
+    return wave_reduce<Op>(v);
+  } else {
+    v = quad_reduce<Op>(v);
+    v = dpp_step<Op, 0x141>(v);
+    if constexpr (LANES >= 16) v = dpp_step<Op, 0x140>(v);
+    if constexpr (LANES >= 32) v = Op::op(v, __shfl_xor(v, 16));
+    return v;
+  }
+}
+// Over a group of LANES lanes or, with 64, of WAVES waves; `slot` is WAVES
+// words of LDS that nobody else uses until the next workgroup barrier.
+template <class Op, int WAVES, int LANES>
 SKG_DEV typename Op::T group_reduce(typename Op::T v, SKG_LDS uint32_t* slot) {
-  v = wave_reduce<Op>(v);
+  v = lanes_reduce<Op, LANES>(v);
   if constexpr (WAVES > 1) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = __builtin_bit_cast(uint32_t, v);
     __syncthreads();

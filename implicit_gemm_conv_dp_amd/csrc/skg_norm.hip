@@ -11,7 +11,10 @@
 //
 // Both read every operand once and keep the row in registers between the
 // reductions, so they are bound by memory traffic, or for a few rows by the
-// latency of one load, one or two reductions and one store.
+// latency of one load, one or two reductions and one store.  A large copy
+// reaches 5.2 to 5.4 TB/s here, two reads and a write 5.8 to 5.9.  Measured:
+// 8192x8192 bf16 with a residual to e4m3 with row scales 81 us (5.8 TB/s), 4864x4096 to bf16
+// 31 us (5.1), gradient of 16384x4096 bf16 with a residual 102 us (5.3).
 #include <exception>
 #include <string>
 
@@ -20,6 +23,9 @@
 
 namespace skg {
 namespace {
+
+// Most workgroups of the gradient, each with a row of partial sums of dw.
+constexpr int kMostGroups = 1024;
 
 enum { OUT_SAME = 0, OUT_E4M3_ROW = 1, OUT_E4M3_MX = 2, OUT_E2M1_MX = 3 };
 
@@ -33,21 +39,68 @@ struct NormParams {
   float eps, inv_cols;
 };
 
-// Weight elements of a chunk, as fp32 (1 without a weight).
-template <int DT>
-SKG_DEV void load_weight(float (&w)[8], const char* p, int w_f32, int e0, int n) {
+// How rows are spread over threads: groups of LANES lanes, or with 64 of
+// WAVES waves, each take whole rows, NCH chunks of eight columns a thread.  A
+// workgroup of 256 threads holds GROUPS groups of a wave or less.
+template <int WAVES_, int LANES_, int NCH_>
+struct Spread {
+  static constexpr int WAVES = WAVES_, LANES = LANES_, NCH = NCH_;
+  static constexpr int SIZE = WAVES * LANES, COLS = SIZE * NCH * 8;
+  static constexpr int THREADS = WAVES == 1 ? 256 : 64 * WAVES;
+  static constexpr int GROUPS = THREADS / SIZE;
+  // Most workgroups of the gradient: 2048 to 4096 waves in flight, and no more
+  // rows of partial sums than that takes (16384x4096 bf16: 512 groups 104 us,
+  // 1024 113, 256 112; 16384x1111: 1024 47 us, 512 70; 4096x16384: 256 112 us,
+  // 128 133).
+  static constexpr int MOST = WAVES >= 8 ? 256 : WAVES == 4 ? 512 : 1024;
+  static_assert(LANES == 64 || WAVES == 1, "a group of several waves has whole ones");
+};
+
+constexpr int kSmallSpread = 64;  // columns of the first spread, the one that rows of less than eight take
+
+// The weights of a thread's columns, as fp32 (1 without a weight).
+template <int DT, class S, int TAIL>
+SKG_DEV void load_weights(float (&w)[S::NCH][8], const char* p, int w_f32, int t, int cols) {
   if (!p) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    for (int i = 0; i < S::NCH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
   } else if (DT == DT_F32 || w_f32) {
-    const Chunk<DT_F32> c = load_chunk<DT_F32>(reinterpret_cast<const uint32_t*>(p) + e0, n);
+    Chunk<DT_F32> c[S::NCH];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = c.get(j);
+    for (int i = 0; i < S::NCH; ++i)
+      c[i] = load_within<DT_F32, TAIL>(reinterpret_cast<const uint32_t*>(p), (t + i * S::SIZE) * 8, cols);
+#pragma unroll
+    for (int i = 0; i < S::NCH; ++i) {
+      place_chunk<DT_F32, TAIL>(c[i], (t + i * S::SIZE) * 8, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = c[i].get(j);
+    }
   } else {
-    const Chunk<DT> c = load_chunk<DT>(reinterpret_cast<const typename Elem<DT>::raw*>(p) + e0, n);
+    Chunk<DT> c[S::NCH];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = c.get(j);
+    for (int i = 0; i < S::NCH; ++i)
+      c[i] = load_within<DT, TAIL>(reinterpret_cast<const typename Elem<DT>::raw*>(p), (t + i * S::SIZE) * 8, cols);
+#pragma unroll
+    for (int i = 0; i < S::NCH; ++i) {
+      place_chunk<DT, TAIL>(c[i], (t + i * S::SIZE) * 8, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = c[i].get(j);
+    }
   }
+}
+// A thread's chunks of one row.
+template <int DT, class S, int TAIL>
+SKG_DEV void load_row(Chunk<DT> (&c)[S::NCH], const char* base, int64_t row, int64_t ld, int t, int cols) {
+  const typename Elem<DT>::raw* p = reinterpret_cast<const typename Elem<DT>::raw*>(base) + row * ld;
+#pragma unroll
+  for (int i = 0; i < S::NCH; ++i) c[i] = load_within<DT, TAIL>(p, (t + i * S::SIZE) * 8, cols);
+}
+template <int DT, class S, int TAIL>
+SKG_DEV void place_row(Chunk<DT> (&c)[S::NCH], int t, int cols) {
+#pragma unroll
+  for (int i = 0; i < S::NCH; ++i) place_chunk<DT, TAIL>(c[i], (t + i * S::SIZE) * 8, cols);
 }
 
 // 1 / sqrt(v) within half an ulp or so: the hardware's reciprocal square
@@ -59,70 +112,26 @@ SKG_DEV float rsqrt_refined(float v) {
   return r > 0.f && v < 3e38f ? n : r;
 }
 
-// One row by a group of 64 * WAVES threads, NCH chunks of eight columns
-// each.  TAIL: the columns are not a multiple of eight.
-template <int DT, int OUT, int WAVES, int NCH, bool TAIL>
-SKG_DEV void norm_row(const NormParams& p, int row, int t, SKG_LDS uint32_t* slots) {
+// What is done with a row once it is summed and stored: y in its type.
+// `slots` are words of LDS that only this row's reductions use.
+template <int DT, int OUT, class S, int TAIL>
+SKG_DEV void norm_output(const NormParams& p, int row, bool live, int t, float s, const Chunk<DT> (&hx)[S::NCH],
+                         const float (&w)[S::NCH][8], SKG_LDS uint32_t* slots) {
   typedef typename Elem<DT>::raw raw;
-  constexpr int G = 64 * WAVES;
-  const raw* x = reinterpret_cast<const raw*>(p.x) + row * p.ldx;
-  Chunk<DT> hx[NCH];
+  constexpr int NCH = S::NCH, G = S::SIZE;
+  // Columns of chunk i that exist, if the row does.
   auto left = [&](int i) {
     const int n = p.cols - (t + i * G) * 8;
-    return TAIL ? n : n > 0 ? 8 : 0;
+    return !live ? 0 : TAIL ? n : n > 0 ? 8 : 0;
   };
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    if (left(i) > 0)
-      hx[i] = load_chunk<DT>(x + (t + i * G) * 8, left(i));
-    else
-      hx[i] = Chunk<DT>{};
-  }
-  if (p.r) {
-    const raw* r = reinterpret_cast<const raw*>(p.r) + row * p.ldr;
-    Chunk<DT> hr[NCH];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      if (left(i) > 0)
-        hr[i] = load_chunk<DT>(r + (t + i * G) * 8, left(i));
-      else
-        hr[i] = Chunk<DT>{};
-    }
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hx[i].put(j, hx[i].get(j) + hr[i].get(j));
-  }
-  if (p.h) {
-    raw* h = reinterpret_cast<raw*>(p.h) + row * p.ldh;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-      if (left(i) > 0) store_chunk<DT>(h + (t + i * G) * 8, left(i), hx[i]);
-  }
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    float part = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) part = __builtin_fmaf(hx[i].get(j), hx[i].get(j), part);
-    sum += part;
-  }
-  sum = group_reduce<OpSum, WAVES>(sum, slots);
-  const float s = rsqrt_refined(sum * p.inv_cols + p.eps);
-  if (p.rstd && t == 0) p.rstd[row] = s;
-
   if constexpr (OUT == OUT_SAME) {
     raw* y = reinterpret_cast<raw*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      if (left(i) > 0) {
-        float w[8];
-        load_weight<DT>(w, p.w, p.w_f32, (t + i * G) * 8, left(i));
-        Chunk<DT> c;
+      Chunk<DT> c;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c.put(j, hx[i].get(j) * s * w[j]);
-        store_chunk<DT>(y + (t + i * G) * 8, left(i), c);
-      }
+      for (int j = 0; j < 8; ++j) c.put(j, hx[i].get(j) * s * w[i][j]);
+      if (left(i) > 0) store_chunk<DT>(y + (t + i * G) * 8, left(i), c);
     }
   } else if constexpr (OUT == OUT_E4M3_ROW) {
     // y / d = h w 448 / max|h w|: the row's factor s cancels, and for
@@ -133,29 +142,22 @@ SKG_DEV void norm_row(const NormParams& p, int row, int t, SKG_LDS uint32_t* slo
     float v[NCH][8];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      float w[8];
-      if (left(i) > 0) {
-        load_weight<DT>(w, p.w, p.w_f32, (t + i * G) * 8, left(i));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.f;
-      }
+    for (int i = 0; i < NCH; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] = hx[i].get(j) * w[j];
-        const uint32_t b = abs_bits(v[i][j]);
-        if (!TAIL || j < left(i)) top = OpMaxBits::op(top, b);
+        v[i][j] = hx[i].get(j) * w[i][j];
+        top = OpMaxBits::op(top, abs_bits(v[i][j]));
       }
-    }
-    top = group_reduce<OpMaxBits, WAVES>(top, slots + WAVES);
+    top = group_reduce<OpMaxBits, S::WAVES, S::LANES>(top, slots);
     const float m = from_bits(top);
     float d = m * s / 448.f;
     // Rows of ordinary size; the others (empty rows, infinities, NaN, and
     // magnitudes whose products leave the range of fp32) take the
     // definition step by step.
     const bool usual = m > 0x1p-100f && m < 0x1p+100f && d >= 0x1p-126f;
-    if (usual) {
+    // The rows of a wave's groups decide together: both reductions need
+    // every lane.
+    if (S::LANES == 64 ? usual : __all(usual)) {
       const float rcp = 1.f / m;
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
@@ -166,25 +168,28 @@ SKG_DEV void norm_row(const NormParams& p, int row, int t, SKG_LDS uint32_t* slo
         }
     } else {
       uint32_t ty = 0;
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        float w[8] = {};
-        if (left(i) > 0) load_weight<DT>(w, p.w, p.w_f32, (t + i * G) * 8, left(i));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i][j] = left(i) > 0 ? hx[i].get(j) * s * w[j] : 0.f;
-          if (!TAIL || j < left(i)) ty = OpMaxBits::op(ty, abs_bits(v[i][j]));
-        }
-      }
-      ty = group_reduce<OpMaxBits, WAVES>(ty, slots + 2 * WAVES);
-      d = from_bits(ty) / 448.f;
-      if (d < 0x1p-126f) d = 0x1p-126f;  // a NaN stays
+      float y[NCH][8];
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] / d;
+        for (int j = 0; j < 8; ++j) {
+          y[i][j] = (t + i * G) * 8 + j < p.cols ? hx[i].get(j) * s * w[i][j] : 0.f;
+          ty = OpMaxBits::op(ty, abs_bits(y[i][j]));
+        }
+      ty = group_reduce<OpMaxBits, S::WAVES, S::LANES>(ty, slots + S::WAVES);
+      float dy = from_bits(ty) / 448.f;
+      if (dy < 0x1p-126f) dy = 0x1p-126f;  // a NaN stays
+      const float rcp = 1.f / m;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float num = v[i][j] * 448.f, q = num * rcp;
+          v[i][j] = usual ? __builtin_fmaf(__builtin_fmaf(-q, m, num), rcp, q) : y[i][j] / dy;
+        }
+      d = usual ? d : dy;
     }
-    if (t == 0) reinterpret_cast<float*>(p.scale)[row] = d;
+    if (t == 0 && live) reinterpret_cast<float*>(p.scale)[row] = d;
     uint8_t* y = reinterpret_cast<uint8_t*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -208,12 +213,11 @@ SKG_DEV void norm_row(const NormParams& p, int row, int t, SKG_LDS uint32_t* slo
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = t + i * G;
-      float w[8], v[8];
+      float v[8];
       uint32_t top = 0;
-      if (left(i) > 0) load_weight<DT>(w, p.w, p.w_f32, c * 8, 8);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = left(i) > 0 ? hx[i].get(j) * s * w[j] : 0.f;
+        v[j] = hx[i].get(j) * s * w[i][j];
         top = OpMaxBits::op(top, abs_bits(v[j]));
       }
       const uint32_t code = mx_code<F4 ? 2 : 8>(quad_reduce<OpMaxBits>(top));
@@ -231,17 +235,60 @@ SKG_DEV void norm_row(const NormParams& p, int row, int t, SKG_LDS uint32_t* slo
   }
 }
 
-template <int DT, int OUT, int WAVES, int NCH>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(NormParams p) {
-  __shared__ uint32_t slots_[3 * WAVES];
+// One row a group: enough workgroups are in flight to hide a row's latencies,
+// and measured no slower than a loop over rows with or without the next
+// row's loads issued ahead (8192x8192 to e4m3: 86 us, 87 and 103).
+template <int DT, int OUT, class S, int TAIL>
+SKG_DEV void norm_row(const NormParams& p, SKG_LDS uint32_t* slots) {
+  typedef typename Elem<DT>::raw raw;
+  constexpr int NCH = S::NCH, G = S::SIZE;
+  const int t = threadIdx.x % G, row = blockIdx.x * S::GROUPS + threadIdx.x / G;
+  const bool live = row < p.rows;  // every lane takes part in the reductions
+  const int from = min(row, p.rows - 1);
+  Chunk<DT> x[NCH], r[NCH];
+  load_row<DT, S, TAIL>(x, p.x, from, p.ldx, t, p.cols);
+  if (p.r) load_row<DT, S, TAIL>(r, p.r, from, p.ldr, t, p.cols);
+  float w[NCH][8];
+  load_weights<DT, S, TAIL>(w, p.w, p.w_f32, t, p.cols);
+  place_row<DT, S, TAIL>(x, t, p.cols);
+  if (p.r) {
+    place_row<DT, S, TAIL>(r, t, p.cols);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i].put(j, x[i].get(j) + r[i].get(j));
+  }
+  if (p.h && live) {
+    raw* h = reinterpret_cast<raw*>(p.h) + row * p.ldh;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int n = p.cols - (t + i * G) * 8;
+      if (n > 0) store_chunk<DT>(h + (t + i * G) * 8, TAIL ? n : 8, x[i]);
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part = __builtin_fmaf(x[i].get(j), x[i].get(j), part);
+    sum += part;
+  }
+  sum = group_reduce<OpSum, S::WAVES, S::LANES>(sum, slots);
+  const float s = rsqrt_refined(sum * p.inv_cols + p.eps);
+  if (p.rstd && t == 0 && live) p.rstd[row] = s;
+  norm_output<DT, OUT, S, TAIL>(p, row, live, t, s, x, w, slots + S::WAVES);
+}
+
+template <int DT, int OUT, class S>
+__global__ __launch_bounds__(S::THREADS) void rmsnorm_kernel(NormParams p) {
+  __shared__ uint32_t slots_[3 * S::WAVES];
   SKG_LDS uint32_t* slots = (SKG_LDS uint32_t*)slots_;
-  const int row = WAVES == 1 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int t = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  if (row >= p.rows) return;  // whole waves, which meet no barrier (WAVES is 1)
-  if (p.cols & 7)
-    norm_row<DT, OUT, WAVES, NCH, true>(p, row, t, slots);
-  else
-    norm_row<DT, OUT, WAVES, NCH, false>(p, row, t, slots);
+  if (!(p.cols & 7)) return norm_row<DT, OUT, S, 0>(p, slots);
+  if constexpr (S::COLS == kSmallSpread) {
+    if (p.cols < 8) return norm_row<DT, OUT, S, 2>(p, slots);
+  }
+  norm_row<DT, OUT, S, 1>(p, slots);
 }
 
 // --- backward ------------------------------------------------------------------
@@ -249,45 +296,37 @@ struct NormBwdParams {
   const char *dy, *h, *w, *dres;
   const float* rstd;
   char* dx;
-  float* partial;  // [groups][cols], or nullptr without dw
-  int rows, cols, w_f32, groups;
+  float* partial;  // [workgroups][cols], or nullptr without dw
+  int rows, cols, w_f32;
   int64_t lddy, ldh, ldr, lddx;
   float inv_cols;
 };
 
-// A group of 64 * WAVES threads takes rows g, g + groups, ...; each thread
-// keeps the sums of dw of its columns.
-template <int DT, int WAVES, int NCH, bool TAIL>
-SKG_DEV void norm_bwd_rows(const NormBwdParams& p, int g, int t, SKG_LDS uint32_t* slots) {
+// Each thread keeps the sums of dw of its columns; the groups of a workgroup
+// are added at the end, in a fixed order, through LDS.
+template <int DT, class S, int TAIL>
+SKG_DEV void norm_bwd_rows(const NormBwdParams& p, SKG_LDS float* lds) {
   typedef typename Elem<DT>::raw raw;
-  constexpr int G = 64 * WAVES;
-  auto left = [&](int i) {
-    const int n = p.cols - (t + i * G) * 8;
-    return TAIL ? n : n > 0 ? 8 : 0;
-  };
+  constexpr int NCH = S::NCH, G = S::SIZE;
+  SKG_LDS uint32_t* slots = (SKG_LDS uint32_t*)lds;
+  const int t = threadIdx.x % G, sub = threadIdx.x / G, step = gridDim.x * S::GROUPS;
   float w[NCH][8], dw[NCH][8];
+  load_weights<DT, S, TAIL>(w, p.w, p.w_f32, t, p.cols);
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
+  for (int i = 0; i < NCH; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = w[i][j] = 0.f;
-    if (left(i) > 0) load_weight<DT>(w[i], p.w, p.w_f32, (t + i * G) * 8, left(i));
-  }
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   int flip = 0;
-  for (int row = g; row < p.rows; row += p.groups, flip ^= WAVES) {
-    const raw* dyp = reinterpret_cast<const raw*>(p.dy) + row * p.lddy;
-    const raw* hp = reinterpret_cast<const raw*>(p.h) + row * p.ldh;
-    const raw* rp = reinterpret_cast<const raw*>(p.dres) + (p.dres ? row * p.ldr : 0);
+  for (int base = blockIdx.x * S::GROUPS; base < p.rows; base += step, flip ^= S::WAVES) {
+    const int row = min(base + sub, p.rows - 1);
+    const bool live = base + sub < p.rows;
     Chunk<DT> dy[NCH], h[NCH], r[NCH];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      dy[i] = h[i] = r[i] = Chunk<DT>{};
-      if (left(i) > 0) {
-        dy[i] = load_chunk<DT>(dyp + (t + i * G) * 8, left(i));
-        h[i] = load_chunk<DT>(hp + (t + i * G) * 8, left(i));
-        if (p.dres) r[i] = load_chunk<DT>(rp + (t + i * G) * 8, left(i));
-      }
-    }
+    load_row<DT, S, TAIL>(dy, p.dy, row, p.lddy, t, p.cols);
+    load_row<DT, S, TAIL>(h, p.h, row, p.ldh, t, p.cols);
+    if (p.dres && p.dx) load_row<DT, S, TAIL>(r, p.dres, row, p.ldr, t, p.cols);
     const float s = p.rstd[row];
+    place_row<DT, S, TAIL>(dy, t, p.cols);
+    place_row<DT, S, TAIL>(h, t, p.cols);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -296,118 +335,131 @@ SKG_DEV void norm_bwd_rows(const NormBwdParams& p, int g, int t, SKG_LDS uint32_
       for (int j = 0; j < 8; ++j) {
         const float n = h[i].get(j) * s;
         part = __builtin_fmaf(dy[i].get(j) * w[i][j], n, part);
-        dw[i][j] = __builtin_fmaf(dy[i].get(j), n, dw[i][j]);
+        dw[i][j] = live ? __builtin_fmaf(dy[i].get(j), n, dw[i][j]) : dw[i][j];
       }
       dot += part;
     }
+    if (!p.dx) continue;
     // Two sets of slots in turn: one barrier a row.
-    dot = group_reduce<OpSum, WAVES>(dot, slots + flip) * p.inv_cols;
-    if (p.dx) {
+    dot = group_reduce<OpSum, S::WAVES, S::LANES>(dot, slots + flip) * p.inv_cols;
+    if (p.dres) place_row<DT, S, TAIL>(r, t, p.cols);
+    if (live) {
       raw* dx = reinterpret_cast<raw*>(p.dx) + row * p.lddx;
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        if (left(i) > 0) {
-          Chunk<DT> c;
+        const int left = p.cols - (t + i * G) * 8;
+        Chunk<DT> c;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float n = h[i].get(j) * s;
-            const float v = s * __builtin_fmaf(-n, dot, dy[i].get(j) * w[i][j]);
-            c.put(j, p.dres ? v + r[i].get(j) : v);
-          }
-          store_chunk<DT>(dx + (t + i * G) * 8, left(i), c);
+        for (int j = 0; j < 8; ++j) {
+          const float n = h[i].get(j) * s;
+          const float v = s * __builtin_fmaf(-n, dot, dy[i].get(j) * w[i][j]);
+          c.put(j, p.dres ? v + r[i].get(j) : v);
         }
+        if (left > 0) store_chunk<DT>(dx + (t + i * G) * 8, TAIL ? left : 8, c);
       }
     }
   }
-  if (p.partial) {
-    float* o = p.partial + (int64_t)g * p.cols;
+  if (!p.partial) return;
+  float* o = p.partial + (int64_t)blockIdx.x * p.cols;
+  if constexpr (S::GROUPS == 1) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      if (left(i) > 0) {
-        Chunk<DT_F32> c;
+      const int left = p.cols - (t + i * G) * 8;
+      Chunk<DT_F32> c;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c.put(j, dw[i][j]);
-        store_chunk<DT_F32>(reinterpret_cast<uint32_t*>(o) + (t + i * G) * 8, left(i), c);
-      }
+      for (int j = 0; j < 8; ++j) c.put(j, dw[i][j]);
+      if (left > 0) store_chunk<DT_F32>(reinterpret_cast<uint32_t*>(o) + (t + i * G) * 8, left, c);
+    }
+  } else {
+    // (The loop of these spreads has no barriers and uses no LDS.)
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lds[sub * S::COLS + (t + i * G) * 8 + j] = dw[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.cols; c += S::THREADS) {
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < S::GROUPS; ++g) sum += lds[g * S::COLS + c];
+      o[c] = sum;
     }
   }
 }
 
-template <int DT, int WAVES, int NCH>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_bwd_kernel(NormBwdParams p) {
-  __shared__ uint32_t slots_[2 * WAVES];
-  SKG_LDS uint32_t* slots = (SKG_LDS uint32_t*)slots_;
-  const int g = WAVES == 1 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int t = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  if (g >= p.groups) return;  // whole waves, which meet no barrier (WAVES is 1)
-  if (p.cols & 7)
-    norm_bwd_rows<DT, WAVES, NCH, true>(p, g, t, slots);
-  else
-    norm_bwd_rows<DT, WAVES, NCH, false>(p, g, t, slots);
+template <int DT, class S>
+__global__ __launch_bounds__(S::THREADS) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  __shared__ float lds[S::GROUPS == 1 ? 2 * S::WAVES : S::GROUPS * S::COLS];
+  if (!(p.cols & 7)) return norm_bwd_rows<DT, S, 0>(p, (SKG_LDS float*)lds);
+  if constexpr (S::COLS == kSmallSpread) {
+    if (p.cols < 8) return norm_bwd_rows<DT, S, 2>(p, (SKG_LDS float*)lds);
+  }
+  norm_bwd_rows<DT, S, 1>(p, (SKG_LDS float*)lds);
 }
 
-// dw[c] = sum over the groups of partial[g][c], in a fixed order: 64 columns
-// by 4 runs of groups a workgroup, then the four runs.  Without groups (no
-// rows) it writes zeros.
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ partial, float* __restrict__ dw, int groups, int cols) {
-  __shared__ float part[4][64];
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float sum = 0.f;
-  if (c < cols)
-    for (int g = run; g < groups; g += 4) sum += partial[(int64_t)g * cols + c];
-  part[run][lane] = sum;
+// dw[c] = sum of the groups' partial[g][c], in a fixed order: 32 columns by 32
+// runs of groups a workgroup, then the runs.  A run's loads are in flight
+// together, so the time is a few latencies however many groups there are
+// (512 x 4096: 4 us; one column a thread over all groups took 32).
+// Without groups (no rows) it writes zeros.
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ partial, float* __restrict__ dw, int groups, int cols) {
+  constexpr int RUNS = 32, MOST = kMostGroups / RUNS;
+  __shared__ float part[RUNS][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = min((int)blockIdx.x * 32 + lane, cols - 1);
+  float v[MOST];
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    const int g = run + k * RUNS;
+    v[k] = g < groups ? partial[(int64_t)g * cols + c] : 0.f;
+  }
+#pragma unroll
+  for (int n = MOST / 2; n; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] += v[k + n];
+  part[run][lane] = v[0];
   __syncthreads();
-  if (run == 0 && c < cols) dw[c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  if (run == 0 && (int)blockIdx.x * 32 + lane < cols) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) sum += part[k][lane];
+    dw[c] = sum;
+  }
 }
 
 // --- host ------------------------------------------------------------------------
 
-// How a row is spread: waves a row and chunks a thread, the first of the
-// list that holds the row.
-struct Spread {
-  int waves, nch;
-};
-constexpr Spread kSpreads[] = {{1, 1}, {1, 2}, {1, 4}, {4, 2}, {4, 4}, {16, 2}, {16, 4}};
-constexpr int kSpreadCount = sizeof(kSpreads) / sizeof(kSpreads[0]);
-int spread_of(int64_t cols) {
-  for (int i = 0; i < kSpreadCount; ++i)
-    if (cols <= int64_t(kSpreads[i].waves) * kSpreads[i].nch * 512) return i;
-  return -1;
+// The first spread of the list that holds the row.
+template <class F, class... S>
+void with_spread(int64_t cols, F&& f, S... spreads) {
+  bool done = false;
+  ((done || cols > decltype(spreads)::COLS ? (void)0 : (f(spreads), (void)(done = true))), ...);
+}
+template <class F>
+void with_spread(int64_t cols, F&& f) {
+  with_spread(cols, f, Spread<1, 8, 1>{}, Spread<1, 16, 1>{}, Spread<1, 32, 1>{}, Spread<1, 64, 1>{}, Spread<1, 64, 2>{},
+              Spread<2, 64, 2>{}, Spread<4, 64, 2>{}, Spread<8, 64, 2>{}, Spread<16, 64, 2>{}, Spread<16, 64, 4>{});
 }
 
-template <int DT, int OUT, int I = 0>
-void launch_norm(const NormParams& p, int spread, hipStream_t st) {
-  if constexpr (I < kSpreadCount) {
-    if (spread == I) {
-      constexpr int W = kSpreads[I].waves, N = kSpreads[I].nch;
-      const unsigned grid = W == 1 ? (unsigned)((p.rows + 3) / 4) : (unsigned)p.rows;
-      hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT, W, N>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, st, p);
-    } else {
-      launch_norm<DT, OUT, I + 1>(p, spread, st);
-    }
+template <int DT, class S>
+void launch_norm(const NormParams& p, int out, hipStream_t st) {
+  const dim3 grid((unsigned)ceil_div(p.rows, S::GROUPS)), block(S::THREADS);
+  switch (out) {
+    case OUT_SAME: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_SAME, S>), grid, block, 0, st, p); break;
+    case OUT_E4M3_ROW: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_ROW, S>), grid, block, 0, st, p); break;
+    case OUT_E4M3_MX: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_MX, S>), grid, block, 0, st, p); break;
+    default: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E2M1_MX, S>), grid, block, 0, st, p);
   }
 }
 template <int DT>
-void launch_norm(const NormParams& p, int out, int spread, hipStream_t st) {
-  switch (out) {
-    case OUT_SAME: return launch_norm<DT, OUT_SAME>(p, spread, st);
-    case OUT_E4M3_ROW: return launch_norm<DT, OUT_E4M3_ROW>(p, spread, st);
-    case OUT_E4M3_MX: return launch_norm<DT, OUT_E4M3_MX>(p, spread, st);
-    default: return launch_norm<DT, OUT_E2M1_MX>(p, spread, st);
-  }
+void launch_norm(const NormParams& p, int out, hipStream_t st) {
+  with_spread(p.cols, [&](auto s) { launch_norm<DT, decltype(s)>(p, out, st); });
 }
-template <int DT, int I = 0>
-void launch_norm_bwd(const NormBwdParams& p, int spread, hipStream_t st) {
-  if constexpr (I < kSpreadCount) {
-    if (spread == I) {
-      constexpr int W = kSpreads[I].waves, N = kSpreads[I].nch;
-      const unsigned grid = W == 1 ? (unsigned)((p.groups + 3) / 4) : (unsigned)p.groups;
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, W, N>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, st, p);
-    } else {
-      launch_norm_bwd<DT, I + 1>(p, spread, st);
-    }
-  }
+template <int DT>
+void launch_norm_bwd(const NormBwdParams& p, int groups, hipStream_t st) {
+  with_spread(p.cols, [&](auto s) {
+    typedef decltype(s) S;
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S>), dim3((unsigned)groups), dim3(S::THREADS), 0, st, p);
+  });
 }
 
 bool row_type(int dt) { return dt == SKG_F16 || dt == SKG_BF16 || dt == SKG_F32; }
@@ -467,13 +519,12 @@ int run_norm(const skg_norm_args_t* a, hipStream_t st) {
   p.eps = a->eps;
   p.inv_cols = 1.f / (float)a->cols;
   const int out = same ? OUT_SAME : a->dtype_y == SKG_F4E2M1 ? OUT_E2M1_MX : a->scale_mode == SKG_SCALE_MX_E8M0 ? OUT_E4M3_MX : OUT_E4M3_ROW;
-  const int spread = spread_of(a->cols);
   if (a->dtype == SKG_F16)
-    launch_norm<DT_F16>(p, out, spread, st);
+    launch_norm<DT_F16>(p, out, st);
   else if (a->dtype == SKG_BF16)
-    launch_norm<DT_BF16>(p, out, spread, st);
+    launch_norm<DT_BF16>(p, out, st);
   else
-    launch_norm<DT_F32>(p, out, spread, st);
+    launch_norm<DT_F32>(p, out, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   return SKG_OK;
@@ -491,10 +542,16 @@ int check_norm_bwd(const skg_norm_bwd_args_t* a) {
   return SKG_OK;
 }
 
-// Groups of rows, each with one row of partial dw sums.
+// Workgroups, each with one row of partial dw sums.
 int bwd_groups(const skg_norm_bwd_args_t* a) {
-  const int64_t most = kSpreads[spread_of(a->cols)].waves == 1 ? 2048 : 512;
-  return (int)(a->rows < most ? a->rows : most);
+  int64_t groups = 0;
+  with_spread(a->cols, [&](auto s) {
+    typedef decltype(s) S;
+    static_assert(S::MOST <= kMostGroups, "what norm_dw_kernel adds");
+    groups = ceil_div(a->rows, S::GROUPS);
+    if (groups > S::MOST) groups = S::MOST;
+  });
+  return (int)groups;
 }
 
 int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStream_t st) {
@@ -526,24 +583,22 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
     p.rows = (int)a->rows;
     p.cols = (int)a->cols;
     p.w_f32 = a->dtype_w == SKG_F32;
-    p.groups = groups;
     p.lddy = a->lddy;
     p.ldh = a->ldh;
     p.ldr = a->lddres;
     p.lddx = a->lddx;
     p.inv_cols = 1.f / (float)a->cols;
-    const int spread = spread_of(a->cols);
-    if (a->dtype == SKG_F16)
-      launch_norm_bwd<DT_F16>(p, spread, st);
+      if (a->dtype == SKG_F16)
+      launch_norm_bwd<DT_F16>(p, groups, st);
     else if (a->dtype == SKG_BF16)
-      launch_norm_bwd<DT_BF16>(p, spread, st);
+      launch_norm_bwd<DT_BF16>(p, groups, st);
     else
-      launch_norm_bwd<DT_F32>(p, spread, st);
+      launch_norm_bwd<DT_F32>(p, groups, st);
     e = hipGetLastError();
     if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   }
   if (a->dw) {
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)ceil_div(a->cols, 64)), dim3(256), 0, st,
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)ceil_div(a->cols, 32)), dim3(1024), 0, st,
                        static_cast<const float*>(ws), a->dw, groups, (int)a->cols);
     e = hipGetLastError();
     if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
