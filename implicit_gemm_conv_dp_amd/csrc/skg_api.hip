@@ -123,8 +123,6 @@ int injected_fault() {
   return INJECT_NONE;
 }
 
-FastDiv make_fastdiv(uint32_t d);
-
 KPlan to_kplan(const skg_plan_t& pl, int inject, int cus) {
   KPlan k;
   k.tiles_m = (int)pl.tiles_m;
@@ -162,16 +160,6 @@ Scratch carve(const skg_plan_t& pl, void* ws) {
     s.ws = reinterpret_cast<float*>(base);
   }
   return s;
-}
-
-FastDiv make_fastdiv(uint32_t d) {
-  FastDiv f;
-  f.d = d;
-  uint32_t s = 0;
-  while ((uint64_t(1) << s) < d) ++s;
-  f.shift = s;
-  f.magic = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
-  return f;
 }
 
 // Checks shared by both run calls once the plan is known: the workspace

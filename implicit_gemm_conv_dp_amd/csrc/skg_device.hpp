@@ -189,6 +189,16 @@ struct FastDiv {
   uint32_t d, magic, shift;
 };
 
+inline FastDiv make_fastdiv(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  f.shift = s;
+  f.magic = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+  return f;
+}
+
 SKG_DEV uint32_t fdiv(uint32_t n, const FastDiv& f) {
   const uint32_t t = __umulhi(n, f.magic);
   return (t + n) >> f.shift;

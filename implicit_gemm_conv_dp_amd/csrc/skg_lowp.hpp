@@ -44,23 +44,15 @@ struct __attribute__((packed, aligned(sizeof(typename C::raw)))) Loose {
   C c;
 };
 
-// n (1 .. 8) elements at p; the others are zero.
-template <int DT>
-SKG_DEV Chunk<DT> load_chunk(const typename Elem<DT>::raw* p, int n) {
-  Chunk<DT> c;
-  if (n >= 8) {
-    c = reinterpret_cast<const Loose<Chunk<DT>>*>(p)->c;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c.v[i] = i < n ? p[i] : 0;
-  }
-  return c;
-}
+// The first n (1 .. 8) elements to p.  The two paths' pointers are kept apart:
+// joined by the compiler, whole chunks too would be stored in pieces (reading
+// 8192x8192 e2m1 codes back took 52 us so, and 32 with whole stores).
 template <int DT>
 SKG_DEV void store_chunk(typename Elem<DT>::raw* p, int n, const Chunk<DT>& c) {
   if (n >= 8) {
     reinterpret_cast<Loose<Chunk<DT>>*>(p)->c = c;
   } else {
+    asm volatile("" : "+v"(p));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = c.v[i];
@@ -91,7 +83,7 @@ SKG_DEV void place_chunk(Chunk<DT>& c, int e0, int cols) {
     uint32_t w[W];
   };
   Words u = __builtin_bit_cast(Words, c);
-  if (TAIL && e0 < cols && e0 + 8 > cols) {
+  if (TAIL && e0 < cols && cols - e0 < 8) {
     const int d = TAIL == 1 ? e0 - (cols - 8) : 0, n = cols - e0;
 #pragma unroll
     for (int b = 4; b >= E; b >>= 1)

@@ -7,6 +7,7 @@
 // are round-to-nearest-even, saturating, of x / 2^(code - 127).  Dividing by a
 // power of two is exact, so each element is rounded once.  A block that
 // holds an infinity or a NaN gets code 255 (NaN) and zero elements.
+#include <algorithm>
 #include <exception>
 #include <string>
 
@@ -24,26 +25,42 @@ struct MxParams {
   int64_t ldx, ldq;        // elements
 };
 
-// Along the rows: a chunk of eight elements a thread, four neighbouring
-// lanes a block.  Bound by memory traffic.
-template <int DT, bool F4>
-__global__ __launch_bounds__(256) void mx_quant_kernel(MxParams p, int64_t chunks, uint32_t cpr) {
+// Along the rows and reading back: U chunks of eight elements a thread, four
+// neighbouring lanes a block.  Chunks are numbered through the lines (fewer
+// than 2^31 a launch); cpr, a multiple of four, is how many a line has.  Bound
+// by memory traffic; U loads in flight a thread keep it streaming.
+struct Walk {
+  uint32_t chunks, cpr;
+  FastDiv div;  // by cpr
+};
+template <int U, class F>
+SKG_DEV void walk_chunks(const Walk& w, F&& f) {
+  static_for<0, U>([&](auto u_) {
+    constexpr int u = decltype(u_)::value;
+    const uint32_t g = (blockIdx.x * U + u) * 256 + threadIdx.x;
+    const uint32_t at = g < w.chunks ? g : w.chunks - 1;
+    const uint32_t line = fdiv(at, w.div);
+    f(u_, g < w.chunks, (int64_t)line, (int)(at - line * w.cpr));
+  });
+}
+
+template <int DT, bool F4, int U, int TAIL>
+SKG_DEV void mx_quant_chunks(const MxParams& p, const Walk& w) {
   typedef typename Elem<DT>::raw raw;
-  // Whole quads of chunks: cpr is a multiple of four.
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t g0 = (int64_t)blockIdx.x * 256; g0 < chunks; g0 += step) {
-    const int64_t g = g0 + threadIdx.x;
-    const bool live = g < chunks;
-    const int64_t row = live ? g / cpr : 0;
-    const int c = (int)(g - row * cpr);
+  Chunk<DT> in[U];
+  walk_chunks<U>(w, [&](auto u, bool, int64_t row, int c) {
+    if (TAIL < 2 || p.cols > 0)
+      in[u] = load_within<DT, TAIL>(reinterpret_cast<const raw*>(p.x) + row * p.ldx, c * 8, (int)p.cols);
+    else
+      in[u] = Chunk<DT>{};
+  });
+  walk_chunks<U>(w, [&](auto u, bool live, int64_t row, int c) {
+    place_chunk<DT, TAIL>(in[u], c * 8, (int)p.cols);
     float v[8];
     uint32_t top = 0;
-    Chunk<DT> in = Chunk<DT>{};
-    const int64_t n = p.cols - (int64_t)c * 8;
-    if (live && n > 0) in = load_chunk<DT>(reinterpret_cast<const raw*>(p.x) + row * p.ldx + (int64_t)c * 8, n < 8 ? (int)n : 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = in.get(j);
+      v[j] = in[u].get(j);
       top = OpMaxBits::op(top, abs_bits(v[j]));
     }
     const uint32_t code = mx_code<F4 ? 2 : 8>(quad_reduce<OpMaxBits>(top));
@@ -57,89 +74,147 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxParams p, int64_t chunk
         store_loose(p.q + row * p.ldq + (int64_t)c * 8, pack_e4m3(v));
       if ((c & 3) == 0) p.sc[row * (p.kq / 32) + (c >> 2)] = (uint8_t)code;
     }
-  }
+  });
+}
+template <int DT, bool F4, int U>
+__global__ __launch_bounds__(256) void mx_quant_kernel(MxParams p, Walk w) {
+  if (!(p.cols & 7)) return mx_quant_chunks<DT, F4, U, 0>(p, w);
+  if (p.cols >= 8) return mx_quant_chunks<DT, F4, U, 1>(p, w);
+  mx_quant_chunks<DT, F4, U, 2>(p, w);
 }
 
-// Along the columns, written transposed: a 128 x 64 tile of x through LDS;
-// thread (column, block) then holds one whole block.
-template <int DT, bool F4>
-__global__ __launch_bounds__(256) void mx_quant_t_kernel(MxParams p) {
+template <int DT, bool F4, int U, bool TAIL>
+SKG_DEV void mx_dequant_chunks(const MxParams& p, const Walk& w) {
   typedef typename Elem<DT>::raw raw;
-  constexpr int TR = 128, TC = 64, PITCH = TC + 8;
-  __shared__ __attribute__((aligned(16))) raw tile[TR * PITCH];
-  const int64_t r0 = (int64_t)blockIdx.x * TR, c0 = (int64_t)blockIdx.y * TC;
-#pragma unroll
-  for (int u = 0; u < TR * TC / 8 / 256; ++u) {
-    const int k = u * 256 + threadIdx.x, r = k / (TC / 8), c = k % (TC / 8) * 8;
-    Chunk<DT> in = Chunk<DT>{};
-    const int64_t n = p.cols - (c0 + c);
-    if (r0 + r < p.rows && n > 0)
-      in = load_chunk<DT>(reinterpret_cast<const raw*>(p.x) + (r0 + r) * p.ldx + c0 + c, n < 8 ? (int)n : 8);
-    *reinterpret_cast<Chunk<DT>*>(&tile[r * PITCH + c]) = in;
-  }
-  __syncthreads();
-  const int col = threadIdx.x >> 2, blk = threadIdx.x & 3;
-  const int64_t k0 = r0 + blk * 32;
-  if (c0 + col >= p.cols || k0 >= p.kq) return;
-  float v[32];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = Elem<DT>::get(tile[(blk * 32 + i) * PITCH + col]);
-    top = OpMaxBits::op(top, abs_bits(v[i]));
-  }
-  const uint32_t code = mx_code<F4 ? 2 : 8>(top);
-  const float inv = mx_inverse(code);
-  uint32_t q[F4 ? 4 : 8];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = code == 255 ? 0.f : v[u * 8 + j] * inv;
-    if constexpr (F4) {
-      q[u] = pack_e2m1(e);
-    } else {
-      const uint2 b = pack_e4m3(e);
-      q[2 * u] = b.x;
-      q[2 * u + 1] = b.y;
-    }
-  }
-  char* o = p.q + (c0 + col) * (F4 ? p.ldq / 2 : p.ldq) + (F4 ? k0 / 2 : k0);
-#pragma unroll
-  for (int u = 0; u < (F4 ? 1 : 2); ++u) store_loose(o + 16 * u, make_uint4(q[4 * u], q[4 * u + 1], q[4 * u + 2], q[4 * u + 3]));
-  p.sc[(c0 + col) * (p.kq / 32) + k0 / 32] = (uint8_t)code;
-}
-
-// Reading back: a chunk of eight codes a thread.
-template <int DT, bool F4>
-__global__ __launch_bounds__(256) void mx_dequant_kernel(MxParams p, int64_t chunks, uint32_t cpr) {
-  typedef typename Elem<DT>::raw raw;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < chunks; g += step) {
-    const int64_t row = g / cpr;
-    const int c = (int)(g - row * cpr);
-    const float d = mx_value(p.sc[row * (p.kq / 32) + (c >> 2)]);
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  uint2 q[U];
+  uint32_t sc[U];
+  walk_chunks<U>(w, [&](auto u, bool, int64_t row, int c) {
+    sc[u] = p.sc[row * (p.kq / 32) + (c >> 2)];
+    if constexpr (F4)
+      q[u].x = load_loose<uint32_t>(p.q + row * (p.ldq / 2) + (int64_t)c * 4);
+    else
+      q[u] = load_loose<uint2>(p.q + row * p.ldq + (int64_t)c * 8);
+  });
+  walk_chunks<U>(w, [&](auto u, bool live, int64_t row, int c) {
+    const float d = mx_value(sc[u]);
     f32x2 v[4];
     if constexpr (F4) {
-      const uint32_t q = load_loose<uint32_t>(p.q + row * (p.ldq / 2) + (int64_t)c * 4);
-      v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
-      v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
-      v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
-      v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+      v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.f, 0);
+      v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.f, 1);
+      v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.f, 2);
+      v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.f, 3);
     } else {
-      const uint2 q = load_loose<uint2>(p.q + row * p.ldq + (int64_t)c * 8);
-      v[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, false);
-      v[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, true);
-      v[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, false);
-      v[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, true);
+      v[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[u].x, false);
+      v[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[u].x, true);
+      v[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[u].y, false);
+      v[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[u].y, true);
     }
     Chunk<DT> out;
 #pragma unroll
     for (int j = 0; j < 8; ++j) out.put(j, v[j >> 1][j & 1] * d);
     const int64_t n = p.cols - (int64_t)c * 8;
-    if (n > 0) store_chunk<DT>(reinterpret_cast<raw*>(const_cast<char*>(p.x)) + row * p.ldx + (int64_t)c * 8, n < 8 ? (int)n : 8, out);
+    if (live && n > 0)
+      store_chunk<DT>(reinterpret_cast<raw*>(const_cast<char*>(p.x)) + row * p.ldx + (int64_t)c * 8,
+                      TAIL && n < 8 ? (int)n : 8, out);
+  });
+}
+template <int DT, bool F4, int U>
+__global__ __launch_bounds__(256) void mx_dequant_kernel(MxParams p, Walk w) {
+  if (p.cols & 7)
+    mx_dequant_chunks<DT, F4, U, true>(p, w);
+  else
+    mx_dequant_chunks<DT, F4, U, false>(p, w);
+}
+
+// Along the columns, written transposed: a 128 x 128 tile of x through LDS
+// (16384x4096 bf16 to e4m3 45 us; 47 with 64 columns, 60 with 32: shorter
+// runs of each row).  A
+// thread then takes eight rows of four columns, so that four neighbouring
+// lanes hold a block of each of the four and sixteen write 128 codes of a
+// line together.  16-bit elements: rows of 136 bytes with groups of four
+// columns exchanged in every other 32 rows put the 64 reads of a wave (16
+// row groups, 4 column groups) on all banks evenly; fp32's 264 do without.
+constexpr int kTRows = 128, kTCols = 128;
+template <int DT>
+struct TTile {
+  static constexpr int TR = kTRows, TC = kTCols, THREADS = TC * 4, ES = sizeof(typename Elem<DT>::raw);
+  static constexpr int P = TC * ES + 8, GB = 4 * ES;  // row pitch, group bytes
+};
+template <int DT, bool F4, int TAIL>
+SKG_DEV void mx_quant_t_tile(const MxParams& p, SKG_LDS char* tile) {
+  typedef typename Elem<DT>::raw raw;
+  typedef TTile<DT> T;
+  constexpr int TR = T::TR, TC = T::TC, ES = T::ES, P = T::P, GB = T::GB;
+  struct Group {
+    raw v[4];
+  };
+  auto at = [&](int r, int g) { return tile + r * P + (ES == 2 ? g ^ ((r >> 5 & 1) << 2) : g) * GB; };
+    // Tiles of the same rows follow one another, so that x's rows are read
+  // through (the other order took 50 us for 42 at 8192x8192 bf16 to e2m1, on
+  // tiles of 64 columns).
+  const uint32_t across = (uint32_t)((p.cols + TC - 1) / TC), down = blockIdx.x / across;
+  const int64_t r0 = (int64_t)down * TR, c0 = (int64_t)(blockIdx.x - down * across) * TC;
+  constexpr int N = TR * TC / 8 / T::THREADS;
+  Chunk<DT> in[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int k = u * T::THREADS + threadIdx.x;
+    const int64_t r = min(r0 + k / (TC / 8), p.rows - 1);
+    if (p.rows > 0)
+      in[u] = load_within<DT, TAIL>(reinterpret_cast<const raw*>(p.x) + r * p.ldx, (int)c0 + k % (TC / 8) * 8, (int)p.cols);
   }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int k = u * T::THREADS + threadIdx.x, r = k / (TC / 8), g = k % (TC / 8) * 2;
+    place_chunk<DT, TAIL>(in[u], (int)c0 + g * 4, (int)p.cols);
+    if (r0 + r >= p.rows) in[u] = Chunk<DT>{};
+    typedef uint32_t words __attribute__((ext_vector_type(GB / 4), aligned(8)));
+    struct Two {
+      words w[2];
+    };
+    const Two two = __builtin_bit_cast(Two, in[u]);
+    *(SKG_LDS words*)at(r, g) = two.w[0];
+    *(SKG_LDS words*)at(r, g + 1) = two.w[1];
+  }
+  __syncthreads();
+  const int oct = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int64_t k0 = r0 + oct * 8;
+  float v[4][8];
+  uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    typedef uint32_t words __attribute__((ext_vector_type(GB / 4), aligned(8)));
+    const Group e = __builtin_bit_cast(Group, *(const SKG_LDS words*)at(oct * 8 + i, grp));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j][i] = Elem<DT>::get(e.v[j]);
+      top[j] = OpMaxBits::op(top[j], abs_bits(v[j][i]));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t line = c0 + grp * 4 + j;
+    const uint32_t code = mx_code<F4 ? 2 : 8>(quad_reduce<OpMaxBits>(top[j]));
+    const float inv = mx_inverse(code);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = code == 255 ? 0.f : v[j][i] * inv;
+    if (line < p.cols && k0 < p.kq) {
+      if constexpr (F4)
+        store_loose(p.q + line * (p.ldq / 2) + k0 / 2, pack_e2m1(v[j]));
+      else
+        store_loose(p.q + line * p.ldq + k0, pack_e4m3(v[j]));
+      if ((oct & 3) == 0) p.sc[line * (p.kq / 32) + k0 / 32] = (uint8_t)code;
+    }
+  }
+}
+
+template <int DT, bool F4>
+__global__ __launch_bounds__(TTile<DT>::THREADS) void mx_quant_t_kernel(MxParams p) {
+  __shared__ __attribute__((aligned(16))) char tile[TTile<DT>::TR * TTile<DT>::P];
+  if (!(p.cols & 7)) return mx_quant_t_tile<DT, F4, 0>(p, (SKG_LDS char*)tile);
+  if (p.cols >= 8) return mx_quant_t_tile<DT, F4, 1>(p, (SKG_LDS char*)tile);
+  mx_quant_t_tile<DT, F4, 2>(p, (SKG_LDS char*)tile);
 }
 
 bool row_type(int dt) { return dt == SKG_F16 || dt == SKG_BF16 || dt == SKG_F32; }
@@ -188,23 +263,43 @@ int run_mx(const skg_mx_args_t* a, bool quant, hipStream_t st) {
       by_fmt(std::integral_constant<int, DT_F32>{});
   };
   if (a->transpose) {
-    const int64_t gx = ceil_div(a->kq, 128), gy = ceil_div(a->cols, 64);
-    if (gy > 65535) return unsupported("too many columns to transpose");
-    const dim3 grid((unsigned)gx, (unsigned)gy);
+    const int64_t tiles = ceil_div(a->kq, kTRows) * ceil_div(a->cols, kTCols);
+    if (tiles > INT32_MAX) return unsupported("too many tiles to transpose");
+    const dim3 grid((unsigned)tiles);
     by_type([&](auto dt, auto f4_) {
-      hipLaunchKernelGGL((mx_quant_t_kernel<decltype(dt)::value, decltype(f4_)::value>), grid, dim3(256), 0, st, p);
+      hipLaunchKernelGGL((mx_quant_t_kernel<decltype(dt)::value, decltype(f4_)::value>), grid, dim3(TTile<decltype(dt)::value>::THREADS), 0, st, p);
     });
   } else {
-    const uint32_t cpr = (uint32_t)(a->kq / 8);
-    const int64_t chunks = a->rows * (int64_t)cpr;
-    const int64_t blocks = ceil_div(chunks, 256);
-    const unsigned grid = (unsigned)(blocks < 65536 ? blocks : 65536);
-    by_type([&](auto dt, auto f4_) {
-      if (quant)
-        hipLaunchKernelGGL((mx_quant_kernel<decltype(dt)::value, decltype(f4_)::value>), dim3(grid), dim3(256), 0, st, p, chunks, cpr);
-      else
-        hipLaunchKernelGGL((mx_dequant_kernel<decltype(dt)::value, decltype(f4_)::value>), dim3(grid), dim3(256), 0, st, p, chunks, cpr);
-    });
+    Walk w;
+    w.cpr = (uint32_t)(a->kq / 8);
+    w.div = make_fastdiv(w.cpr);
+    // Lines in launches of fewer than 2^31 chunks.
+    const int64_t most = std::max<int64_t>(1, (INT32_MAX - 4095) / w.cpr);
+    for (int64_t r0 = 0; r0 < a->rows; r0 += most) {
+      const int64_t n = std::min<int64_t>(most, a->rows - r0);
+      w.chunks = (uint32_t)(n * w.cpr);
+      MxParams q = p;
+      q.rows = n;
+      q.x += r0 * a->ldx * elem_bytes(a->dtype);
+      q.q += row_bytes(a->dtype_q, r0 * a->ldq);
+      q.sc += r0 * (a->kq / 32);
+      // Many chunks: four a thread (8192x8192 bf16 to e2m1 33 us, 5.2 TB/s,
+      // and back 32).  Few: one, for the sake of more workgroups.
+            const int u = w.chunks >= (1u << 20) ? 4 : 1;
+      const dim3 grid((unsigned)ceil_div(w.chunks, 256 * u));
+      by_type([&](auto dt, auto f4_) {
+        constexpr int DT = decltype(dt)::value;
+        constexpr bool F4 = decltype(f4_)::value;
+        if (quant && u == 4)
+          hipLaunchKernelGGL((mx_quant_kernel<DT, F4, 4>), grid, dim3(256), 0, st, q, w);
+        else if (quant)
+          hipLaunchKernelGGL((mx_quant_kernel<DT, F4, 1>), grid, dim3(256), 0, st, q, w);
+        else if (u == 4)
+          hipLaunchKernelGGL((mx_dequant_kernel<DT, F4, 4>), grid, dim3(256), 0, st, q, w);
+        else
+          hipLaunchKernelGGL((mx_dequant_kernel<DT, F4, 1>), grid, dim3(256), 0, st, q, w);
+      });
+    }
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
