@@ -43,13 +43,25 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "skg_run_mx_dequant"]
 
 
-def _enum(table, v, what):
-    r = table.get(v)
-    if r is None:
+class _Names(dict):
+    """The values of a table's names; whole numbers stand for themselves."""
+
+    def __init__(self, table, what):
+        super().__init__(table)
+        self.what = what
+
+    def __missing__(self, v):
         if isinstance(v, int):
             return v
-        raise ValueError("unknown %s %r" % (what, v))
-    return r
+        raise ValueError("unknown %s %r" % (self.what, v))
+
+
+_DTYPE = _Names(DTYPES, "dtype")
+_TILE = _Names(TILES, "tile")
+_MODE = _Names(MODES, "mode")
+_REDUCTION = _Names(REDUCTIONS, "reduction")
+_SCALE_MODE = _Names(SCALE_MODES, "scale mode")
+_SK_ORDER = _Names(SK_ORDERS, "stream-K order")
 
 
 def _ptr(t):
@@ -62,13 +74,13 @@ def gemm_args(A=None, B=None, C=None, *, M, N, K, dtype_ab, dtype_c, lda=None, l
     # Positional, in the struct's order: a call for a few tokens spends more
     # time here than on the GPU.
     return _lib.skg_gemm_args_t(
-        M, N, K, _enum(DTYPES, dtype_ab, "dtype"), _enum(DTYPES, dtype_c, "dtype"),
-        _ptr(A), K if lda is None else lda, _ptr(B), K if ldb is None else ldb,
-        _ptr(C), N if ldc is None else ldc, _ptr(scale_a), _ptr(scale_b),
-        _lib.TILE_AUTO if tile == "auto" else _enum(TILES, tile, "tile"),
-        _enum(MODES, mode, "mode"), _enum(REDUCTIONS, reduction, "reduction"), ctas,
-        _enum(SCALE_MODES, scale_mode, "scale mode"),
-        _enum(SK_ORDERS, sk_order, "stream-K order"))
+        M, N, K, _DTYPE[dtype_ab], _DTYPE[dtype_c],
+        0 if A is None else A.data_ptr(), K if lda is None else lda,
+        0 if B is None else B.data_ptr(), K if ldb is None else ldb,
+        0 if C is None else C.data_ptr(), N if ldc is None else ldc,
+        0 if scale_a is None else scale_a.data_ptr(), 0 if scale_b is None else scale_b.data_ptr(),
+        _lib.TILE_AUTO if tile == "auto" else _TILE[tile], _MODE[mode], _REDUCTION[reduction],
+        ctas, _SCALE_MODE[scale_mode], _SK_ORDER[sk_order])
 
 
 def wgrad_args(x=None, dy=None, dw=None, *, n, h, w, c, k, r, s, stride=(1, 1), pad=(0, 0),
@@ -78,13 +90,13 @@ def wgrad_args(x=None, dy=None, dw=None, *, n, h, w, c, k, r, s, stride=(1, 1), 
     a.stride_h, a.stride_w = stride
     a.pad_h, a.pad_w = pad
     a.groups = groups
-    a.dtype = _enum(DTYPES, dtype, "dtype")
+    a.dtype = _DTYPE[dtype]
     a.x, a.dy, a.dw = _ptr(x), _ptr(dy), _ptr(dw)
-    a.tile_id = _enum(TILES, tile, "tile")
-    a.mode = _enum(MODES, mode, "mode")
-    a.reduction = _enum(REDUCTIONS, reduction, "reduction")
+    a.tile_id = _TILE[tile]
+    a.mode = _MODE[mode]
+    a.reduction = _REDUCTION[reduction]
     a.ctas = ctas
-    a.sk_order = _enum(SK_ORDERS, sk_order, "stream-K order")
+    a.sk_order = _SK_ORDER[sk_order]
     return a
 
 
@@ -97,14 +109,14 @@ def conv_args(act=None, filt=None, out=None, *, n, h, w, c, k, r, s, stride=(1, 
     a.stride_h, a.stride_w = stride
     a.pad_h, a.pad_w = pad
     a.groups = groups
-    a.dtype = _enum(DTYPES, dtype, "dtype")
-    a.dtype_out = _enum(DTYPES, dtype_out, "dtype")
+    a.dtype = _DTYPE[dtype]
+    a.dtype_out = _DTYPE[dtype_out]
     a.act, a.filt, a.out = _ptr(act), _ptr(filt), _ptr(out)
-    a.tile_id = _enum(TILES, tile, "tile")
-    a.mode = _enum(MODES, mode, "mode")
-    a.reduction = _enum(REDUCTIONS, reduction, "reduction")
+    a.tile_id = _TILE[tile]
+    a.mode = _MODE[mode]
+    a.reduction = _REDUCTION[reduction]
     a.ctas = ctas
-    a.sk_order = _enum(SK_ORDERS, sk_order, "stream-K order")
+    a.sk_order = _SK_ORDER[sk_order]
     return a
 
 
@@ -212,25 +224,34 @@ def dgrad(dy, filt, dx, workspace=None, stream=None, **kw):
 def rmsnorm_args(x=None, y=None, *, rows, cols, dtype, dtype_y=None, weight=None, dtype_w=None,
                  residual=None, h=None, rstd=None, y_scale=None, scale_mode="rowcol", eps=1e-5,
                  ldx=None, ldr=None, ldh=None, ldy=None):
-    dt = _enum(DTYPES, dtype, "dtype")
+    dt = _DTYPE[dtype]
     return _lib.skg_norm_args_t(
-        rows, cols, dt, dt if dtype_w is None else _enum(DTYPES, dtype_w, "dtype"),
-        dt if dtype_y is None else _enum(DTYPES, dtype_y, "dtype"),
-        _enum(SCALE_MODES, scale_mode, "scale mode"), _ptr(x), cols if ldx is None else ldx,
-        _ptr(residual), cols if ldr is None else ldr, _ptr(weight), _ptr(h),
-        cols if ldh is None else ldh, _ptr(y), cols if ldy is None else ldy, _ptr(y_scale),
-        _ptr(rstd), eps)
+        rows, cols, dt,
+        dt if dtype_w is None else _DTYPE[dtype_w],
+        dt if dtype_y is None else _DTYPE[dtype_y],
+        _SCALE_MODE[scale_mode],
+        0 if x is None else x.data_ptr(), cols if ldx is None else ldx,
+        0 if residual is None else residual.data_ptr(), cols if ldr is None else ldr,
+        0 if weight is None else weight.data_ptr(),
+        0 if h is None else h.data_ptr(), cols if ldh is None else ldh,
+        0 if y is None else y.data_ptr(), cols if ldy is None else ldy,
+        0 if y_scale is None else y_scale.data_ptr(),
+        0 if rstd is None else rstd.data_ptr(), eps)
 
 
 def rmsnorm_bwd_args(dy=None, h=None, rstd=None, dx=None, *, rows, cols, dtype, weight=None,
                      dtype_w=None, dres=None, dw=None, lddy=None, ldh=None, lddres=None,
                      lddx=None):
-    dt = _enum(DTYPES, dtype, "dtype")
+    dt = _DTYPE[dtype]
     return _lib.skg_norm_bwd_args_t(
-        rows, cols, dt, dt if dtype_w is None else _enum(DTYPES, dtype_w, "dtype"),
-        _ptr(dy), cols if lddy is None else lddy, _ptr(h), cols if ldh is None else ldh,
-        _ptr(rstd), _ptr(weight), _ptr(dres), cols if lddres is None else lddres, _ptr(dx),
-        cols if lddx is None else lddx, _ptr(dw))
+        rows, cols, dt, dt if dtype_w is None else _DTYPE[dtype_w],
+        0 if dy is None else dy.data_ptr(), cols if lddy is None else lddy,
+        0 if h is None else h.data_ptr(), cols if ldh is None else ldh,
+        0 if rstd is None else rstd.data_ptr(),
+        0 if weight is None else weight.data_ptr(),
+        0 if dres is None else dres.data_ptr(), cols if lddres is None else lddres,
+        0 if dx is None else dx.data_ptr(), cols if lddx is None else lddx,
+        0 if dw is None else dw.data_ptr())
 
 
 def mx_args(x=None, q=None, scales=None, *, rows, cols, dtype, dtype_q, kq=None, ldx=None,
@@ -238,9 +259,10 @@ def mx_args(x=None, q=None, scales=None, *, rows, cols, dtype, dtype_q, kq=None,
     if kq is None:
         kq = ((rows if transpose else cols) + 31) // 32 * 32
     return _lib.skg_mx_args_t(
-        rows, cols, kq, _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, dtype_q, "dtype"), _ptr(x),
-        cols if ldx is None else ldx, _ptr(q), kq if ldq is None else ldq, _ptr(scales),
-        1 if transpose else 0)
+        rows, cols, kq, _DTYPE[dtype], _DTYPE[dtype_q],
+        0 if x is None else x.data_ptr(), cols if ldx is None else ldx,
+        0 if q is None else q.data_ptr(), kq if ldq is None else ldq,
+        0 if scales is None else scales.data_ptr(), 1 if transpose else 0)
 
 
 def rmsnorm(x, y, stream=None, **kw):

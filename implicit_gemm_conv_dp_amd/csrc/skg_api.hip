@@ -24,7 +24,7 @@ struct DeviceRec {
   bool valid = false;
   bool gfx950 = false;
   int cus = 0;
-  std::string arch;
+  char arch[64] = {};
 };
 
 std::mutex g_dev_mu;
@@ -45,8 +45,8 @@ int current_device(DeviceRec* out) {
     hipDeviceProp_t prop;
     e = hipGetDeviceProperties(&prop, dev);
     if (e != hipSuccess) return hip_failure(std::string("hipGetDeviceProperties: ") + hipGetErrorString(e));
-    r.arch = prop.gcnArchName;
-    r.gfx950 = r.arch.compare(0, 6, "gfx950") == 0;
+    std::strncpy(r.arch, prop.gcnArchName, sizeof(r.arch) - 1);
+    r.gfx950 = std::strncmp(r.arch, "gfx950", 6) == 0;
     r.cus = prop.multiProcessorCount;
     r.valid = true;
   }
@@ -59,7 +59,7 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   DeviceRec d;
   int rc = current_device(&d);
   if (rc) return rc;
-  if (!d.gfx950) return unsupported("unsupported arch " + d.arch + " (the engine is built for gfx950)");
+  if (!d.gfx950) return unsupported(std::string("unsupported arch ") + d.arch + " (the engine is built for gfx950)");
   // The runtime's answer for an instance does not change: asked for once.
   struct Known {
     int op, tile, dtype, occ;
@@ -480,7 +480,7 @@ int check_device(int* cus) {
   DeviceRec d;
   const int rc = current_device(&d);
   if (rc) return rc;
-  if (!d.gfx950) return unsupported("unsupported arch " + d.arch + " (the engine is built for gfx950)");
+  if (!d.gfx950) return unsupported(std::string("unsupported arch ") + d.arch + " (the engine is built for gfx950)");
   *cus = d.cus;
   return SKG_OK;
 }
