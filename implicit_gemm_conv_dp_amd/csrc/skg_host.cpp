@@ -332,13 +332,15 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
 
 // The fp4 tile of a call that leaves it open: the least of the times that these
 // models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
-// 8192, K 512 to 8192) on all tiles, each within 15 % or so of the measured.
-// - A direct tile's workgroups read their operands' rows at 30 kB/us a CU,
-//   whatever its shape: 1x8192x8192 8.3 us on 16x16 (12.7 on 16x64),
-//   48x4863x4096 8.3 on 16x64 (11.3 on 16x16), 1024x1024x1024 6.3 on 64x64
-//   (9.5 on 16x32).
+// 8192, K 256 to 8192) on all tiles, most within 15 % of the measured.
+// - A direct tile's workgroups take their operands' rows in at 60 kB/us a CU,
+//   the larger ones after a start that nothing covers (one workgroup a CU),
+//   and short reductions cost a round of workgroups its latency:
+//   48x4863x4096 5.3 us on 16x32 (6.1 on 16x16, 8.0 on 64x64), 64x8192x8192
+//   9.6 on 32x64 (10.8 on 32x32, 14.3 on 16x32), 1024x1024x8192 13.1 on 64x64
+//   (19.3 on 128x128, 19.5 on 32x32).
 // - A ring tile costs a start and end and its iterations, a workgroup a CU at
-//   a time: 256x8192x8192 21.4 us on 128x128 (43.0 on direct 64x64, 48.4 on
+//   a time: 512x8192x1024 9.2 us on 128x128 (20.0 on direct 64x64, 15.2 on
 //   256x256), 4096x4096x1024 22.2 on 256x256 (25.9 on 128x128).
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   skg_gemm_args_t r = *a;
@@ -354,7 +356,9 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
     double us;
     if (t.direct) {
       const int64_t rows = std::min<int64_t>(t.tm, r.M) + std::min<int64_t>(t.tn, r.N);
-      us = 2.2 + rounds * (double)rows * (double)r.K * (0.5 + 1.0 / 32) / 30e3;
+      const double bytes = (double)rows * (double)r.K * (0.5 + 1.0 / 32);
+      const double start = std::max(0, t.tm + t.tn - 64) * 0.036, least = (t.tm + t.tn - 18) * 0.04;
+      us = 1.6 + rounds * std::max(bytes / 60e3 + start, least);
     } else {
       const double iters = (double)ceil_div(r.K, t.tk);
       us = rounds * (t.tm == 256 ? 12 + 1.5 * iters : 5 + 0.45 * iters);

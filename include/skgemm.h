@@ -226,9 +226,8 @@ enum skg_tile {
                                 iteration, 4 waves */
   SKG_TILE_256x256x256 = 9,  /* fp4 GEMM with MX block scales, 4 waves */
   SKG_TILE_128x128x256 = 10, /* fp4 GEMM with MX block scales, 4 waves */
-  /* fp4 GEMM with MX block scales, 4 waves that split the reduction (512
-     elements of K among them) and read their operands straight into
-     registers; mode dp or auto, no workspace */
+  /* fp4 GEMM with MX block scales, for few tiles: 4 waves that split the
+     reduction; mode dp or auto, no workspace */
   SKG_TILE_16x16x512 = 11,
   SKG_TILE_16x32x512 = 12,
   SKG_TILE_16x64x512 = 13,
