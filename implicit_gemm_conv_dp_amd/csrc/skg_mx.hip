@@ -78,9 +78,10 @@ SKG_DEV void mx_quant_chunks(const MxParams& p, const Walk& w) {
 }
 template <int DT, bool F4, int U>
 __global__ __launch_bounds__(256) void mx_quant_kernel(MxParams p, Walk w) {
-  if (!(p.cols & 7)) return mx_quant_chunks<DT, F4, U, 0>(p, w);
-  if (p.cols >= 8) return mx_quant_chunks<DT, F4, U, 1>(p, w);
-  mx_quant_chunks<DT, F4, U, 2>(p, w);
+  // (No columns at all, only padding to write, belongs with less than eight.)
+  if (p.cols < 8) return mx_quant_chunks<DT, F4, U, 2>(p, w);
+  if (p.cols & 7) return mx_quant_chunks<DT, F4, U, 1>(p, w);
+  mx_quant_chunks<DT, F4, U, 0>(p, w);
 }
 
 template <int DT, bool F4, int U, bool TAIL>
@@ -231,7 +232,8 @@ int run_mx(const skg_mx_args_t* a, bool quant, hipStream_t st) {
   if (a->kq < axis || a->kq % 32) return unsupported("kq must be a multiple of 32 and cover the quantised axis");
   if (a->ldx < a->cols || a->ldq < a->kq) return unsupported("leading dimension too small");
   if (f4 && a->ldq % 2) return unsupported("ldq of e2m1 codes must be even");
-  if (a->rows > INT32_MAX || a->cols > INT32_MAX || a->kq > INT32_MAX) return unsupported("dimension too large");
+  const int64_t most = INT32_MAX - 4096;  // rounded up to tiles within 32 bits
+  if (a->rows > most || a->cols > most || a->kq > most) return unsupported("dimension too large");
   if (lines == 0 || a->kq == 0) return SKG_OK;
   const bool reads = quant ? axis > 0 : true;
   if ((!a->x && reads && a->cols > 0) || !a->q || !a->scales) return unsupported("null x, q or scales");

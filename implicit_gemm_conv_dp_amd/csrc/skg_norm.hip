@@ -26,6 +26,8 @@ namespace {
 
 // Most workgroups of the gradient, each with a row of partial sums of dw.
 constexpr int kMostGroups = 1024;
+// Rows and what they are rounded up to or stepped by stay within 32 bits.
+constexpr int64_t kMostRows = INT32_MAX - 65536;
 
 enum { OUT_SAME = 0, OUT_E4M3_ROW = 1, OUT_E4M3_MX = 2, OUT_E2M1_MX = 3 };
 
@@ -476,7 +478,7 @@ int check_norm(const skg_norm_args_t* a) {
   if (!same && !mx && a->scale_mode != SKG_SCALE_ROWCOL) return unsupported("the norm's scales are one a row or MX blocks");
   if (f4 && !mx) return unsupported("e2m1 output needs MX block scales");
   if (a->rows < 0 || a->cols <= 0) return unsupported("rows must not be negative and cols must be positive");
-  if (a->rows > INT32_MAX) return unsupported("too many rows");
+  if (a->rows > kMostRows) return unsupported("too many rows");
   if (a->cols > SKG_NORM_MAX_COLS) return unsupported("rows longer than SKG_NORM_MAX_COLS");
   if (!same && mx && a->cols % 32) return unsupported("MX output needs cols to be a multiple of 32");
   if (a->ldx < a->cols || (a->residual && a->ldr < a->cols) || (a->h && a->ldh < a->cols) || a->ldy < a->cols)
@@ -535,7 +537,7 @@ int check_norm_bwd(const skg_norm_bwd_args_t* a) {
   if (!row_type(a->dtype)) return unsupported("the norm's rows are f16, bf16 or f32");
   if (a->dtype_w != a->dtype && a->dtype_w != SKG_F32) return unsupported("the weight has the rows' type or f32");
   if (a->rows < 0 || a->cols <= 0) return unsupported("rows must not be negative and cols must be positive");
-  if (a->rows > INT32_MAX) return unsupported("too many rows");
+  if (a->rows > kMostRows) return unsupported("too many rows");
   if (a->cols > SKG_NORM_MAX_COLS) return unsupported("rows longer than SKG_NORM_MAX_COLS");
   if (a->lddy < a->cols || a->ldh < a->cols || (a->dres && a->lddres < a->cols) || (a->dx && a->lddx < a->cols))
     return unsupported("leading dimension too small");

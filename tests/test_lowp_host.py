@@ -167,3 +167,32 @@ def test_fp4_plan():
     p = plan(M=300, N=520, K=640)()
     assert (p["tm"], p["tn"], p["tk"], p["tiles_m"], p["tiles_n"], p["iters_per_tile"]) == \
         (256, 256, 256, 2, 3, 3)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(tile="16x16x512", mode="dp_sk", reduction="tree"), "splits K"),
+    (dict(tile="64x64x512", mode="splitk", reduction="linear"), "splits K"),
+    (dict(tile="32x32x512", mode="persistent"), "splits K"),
+    (dict(tile="16x16x512", scale_mode="rowcol"), "MX"),
+])
+def test_direct_tile_refusals(kw, word):
+    refused(plan(**kw), word)
+
+
+def test_direct_plan():
+    p = plan(M=20, N=70, K=1152, ldc=72, tile="16x32x512", mode="auto")()
+    assert (p["tm"], p["tn"], p["tk"], p["tiles_m"], p["tiles_n"], p["iters_per_tile"]) == (16, 32, 512, 2, 3, 3)
+    assert p["workspace_bytes"] == 0 and p["sk_ctas"] == 0 and p["grid"] == 6
+    assert p["mode"] == skg.MODES["dp"] and p["requested_mode"] == skg.MODES["auto"]
+
+
+def test_auto_tile():
+    """Small tiles for few rows, large ones for many, never a workspace; a
+    stream-K mode takes a tile that has it."""
+    for (M, N, K), most in (((1, 4096, 4096), 16), ((48, 4863, 4096), 48), ((200, 300, 512), 32)):
+        p = plan(M=M, N=N, K=K, ldc=-(-N // 8) * 8, tile="auto", mode="auto")()
+        assert p["tm"] <= most and p["tn"] <= 64 and p["workspace_bytes"] == 0
+    p = plan(M=8192, N=8192, K=8192, tile="auto", mode="auto")()
+    assert (p["tm"], p["tn"]) == (256, 256) and p["mode"] == skg.MODES["dp"]
+    p = plan(M=48, N=4864, K=4096, tile="auto", mode="dp_sk", reduction="tree", ctas=64)()
+    assert p["tm"] >= 128 and p["sk_ctas"] == 64
