@@ -22,7 +22,8 @@ tile="auto")`` for their product.
 
 from . import _lib
 from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  # noqa: F401
-                   skg_plan_wgrad, skg_profile_events, skg_run_gemm, skg_run_wgrad,
+                   skg_plan_run_gemm, skg_plan_wgrad, skg_profile_events, skg_run_gemm,
+                   skg_run_wgrad,
                    skg_tile_info, skg_gemm_workspace_bytes, skg_wgrad_workspace_bytes,
                    skg_fixup_timeouts, skg_run_wgrad_static, skg_plan_fwd, skg_plan_dgrad,
                    skg_run_fwd, skg_run_dgrad, skg_run_rmsnorm, skg_run_rmsnorm_bwd,
@@ -34,7 +35,7 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "workspace_for", "SkgError", "MODES", "REDUCTIONS", "DTYPES", "TILES", "SCALE_MODES",
            "SK_ORDERS",
            "skg_default_pool", "skg_device_info", "skg_plan_gemm", "skg_plan_wgrad",
-           "skg_run_gemm", "skg_run_wgrad", "skg_tile_info", "skg_profile_events",
+           "skg_run_gemm", "skg_plan_run_gemm", "skg_run_wgrad", "skg_tile_info", "skg_profile_events",
            "skg_gemm_workspace_bytes", "skg_wgrad_workspace_bytes", "skg_fixup_timeouts",
            "skg_run_wgrad_static", "skg_plan_fwd", "skg_plan_dgrad", "skg_run_fwd",
            "skg_run_dgrad", "rmsnorm", "rmsnorm_bwd", "mx_quant", "mx_dequant",
@@ -190,7 +191,13 @@ def gemm(A, B, C, scale_a=None, scale_b=None, workspace=None, stream=None, **kw)
     """Enqueue C = epilogue(A @ B) on ``stream`` (default: torch's current
     stream).  Returns the plan (a dict)."""
     args = gemm_args(A, B, C, scale_a=scale_a, scale_b=scale_b, **kw)
-    plan = skg_plan_gemm(args).as_dict()
+    if workspace is None:
+        plan, launched = skg_plan_run_gemm(args, 0, 0, _handle(stream))
+        plan = plan.as_dict()
+        if launched:
+            return plan
+    else:
+        plan = skg_plan_gemm(args).as_dict()
     _run(skg_run_gemm, args, plan, C.device, workspace, stream)
     return plan
 

@@ -143,6 +143,10 @@ EXPORTS = {
                                        ctypes.POINTER(ctypes.c_int32)]),
     "skg_plan_gemm": (ctypes.c_int, [ctypes.POINTER(skg_gemm_args_t), ctypes.POINTER(skg_plan_t)]),
     "skg_plan_wgrad": (ctypes.c_int, [ctypes.POINTER(skg_wgrad_args_t), ctypes.POINTER(skg_plan_t)]),
+    "skg_plan_run_gemm": (ctypes.c_int, [ctypes.POINTER(skg_gemm_args_t), ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_void_p,
+                                         ctypes.POINTER(skg_plan_t),
+                                         ctypes.POINTER(ctypes.c_int32)]),
     "skg_run_gemm": (ctypes.c_int, [ctypes.POINTER(skg_gemm_args_t), ctypes.c_void_p,
                                     ctypes.c_size_t, ctypes.c_void_p]),
     "skg_run_wgrad": (ctypes.c_int, [ctypes.POINTER(skg_wgrad_args_t), ctypes.c_void_p,
@@ -247,6 +251,14 @@ def skg_plan_wgrad(args):
 
 def skg_run_gemm(args, ws_ptr, ws_bytes, stream_ptr):
     return check(load().skg_run_gemm(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))
+
+
+def skg_plan_run_gemm(args, ws_ptr, ws_bytes, stream_ptr):
+    """(plan, whether it was launched)."""
+    out, launched = skg_plan_t(), ctypes.c_int32()
+    check(load().skg_plan_run_gemm(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr,
+                                   ctypes.byref(out), ctypes.byref(launched)))
+    return out, launched.value
 
 
 def skg_run_wgrad(args, ws_ptr, ws_bytes, stream_ptr):

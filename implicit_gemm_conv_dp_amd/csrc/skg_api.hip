@@ -474,6 +474,71 @@ int run_conv(const skg_conv_args_t* a, bool dgrad, void* ws, size_t ws_bytes, hi
   return SKG_OK;
 }
 
+// out, launched: the plan is wanted, and a workspace too small for it is not
+// an error but leaves the call undone.
+int run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream, skg_plan_t* out, int32_t* launched) {
+  if (!args) return unsupported("null arguments");
+  const skg_gemm_args_t resolved = resolve_gemm(args), *a = &resolved;
+  int rc = validate_gemm(a);
+  if (rc) return rc;
+  if (!a->A || !a->B || !a->C) return unsupported("null A, B or C");
+  if (!aligned(a->A, 16) || !aligned(a->B, 16) || !aligned(a->C, 16))
+    return unsupported("A, B and C must be 16-byte aligned");
+  if ((a->scale_a && !aligned(a->scale_a, 16)) || (a->scale_b && !aligned(a->scale_b, 16)))
+    return unsupported("scales must be 16-byte aligned");
+  const TileDesc* t = tile_desc(a->tile_id);
+  if (a->scale_mode == SKG_SCALE_MX_E8M0 && (!a->scale_a || !a->scale_b))
+    return unsupported("MX block scales need both scale arrays");
+  GemmInst inst = gemm_instance(a->tile_id, a->dtype_ab, a->scale_mode);
+  if (!inst.launch) return unsupported("no GEMM instance for this tile and dtype");
+  int cus = 0, per_cu = 0;
+  rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu);
+  if (rc) return rc;
+  skg_plan_t pl;
+  rc = plan_launch(gemm_shape(a, *t), *t, a->mode, a->reduction, a->ctas,
+                   resolve_sk_order(a->sk_order, false), cus, per_cu, &pl);
+  if (rc) return rc;
+  if (out) *out = pl;
+  if (launched) {
+    *launched = (size_t)pl.workspace_bytes <= ws_bytes;
+    if (!*launched) return SKG_OK;
+  }
+  rc = check_run(pl, ws, ws_bytes, cus, per_cu);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a->dtype_ab == SKG_F4E2M1 && pl.reduction != SKG_RED_ATOMIC) {
+    // Kernel resets, so that the call may be captured into a graph.
+    const size_t bytes = !pl.sk_ctas ? 0 : (size_t)(handoff_reduction(pl.reduction) ? pl.flags_bytes : pl.workspace_bytes);
+    hipError_t e = zero_fill(ws, bytes, st);
+    if (e != hipSuccess) return hip_failure(std::string("reset: ") + hipGetErrorString(e));
+  } else {
+    rc = reset_scratch(pl, ws, st);
+    if (rc) return rc;
+  }
+  if (pl.reduction == SKG_RED_ATOMIC && pl.sk_ctas) {
+    hipError_t e = hipMemset2DAsync(a->C, (size_t)a->ldc * 4, 0, (size_t)a->N * 4, (size_t)a->M, st);
+    if (e != hipSuccess) return hip_failure(std::string("zeroing C: ") + hipGetErrorString(e));
+  }
+  GemmParams g;
+  g.A = static_cast<const char*>(a->A);
+  g.B = static_cast<const char*>(a->B);
+  g.C = static_cast<char*>(a->C);
+  g.M = (int)a->M;
+  g.N = (int)a->N;
+  g.K = (int)a->K;
+  g.lda_b = (uint32_t)row_bytes(a->dtype_ab, a->lda);
+  g.ldb_b = (uint32_t)row_bytes(a->dtype_ab, a->ldb);
+  g.ldc = (int)a->ldc;
+  g.sa = a->scale_a;
+  g.sb = a->scale_b;
+  g.dtype_c = a->dtype_c == SKG_F32 ? DT_F32 : (a->dtype_c == SKG_F16 ? DT_F16 : DT_BF16);
+  const int inject = injected_fault();
+  if (inject == INJECT_LAUNCH) return hip_failure("launch: failure injected by SKG_FAULT=launch");
+  hipError_t e = inst.launch(g, to_kplan(pl, inject, cus), carve(pl, ws), st, g_ev_start, g_ev_stop);
+  if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
+  return SKG_OK;
+}
+
 }  // namespace
 
 int check_device(int* cus) {
@@ -605,61 +670,21 @@ int skg_fixup_timeouts(uint32_t* count, int32_t reset) {
 int skg_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream) {
   try {
     clear_error();
-    if (!args) return unsupported("null arguments");
-    const skg_gemm_args_t resolved = resolve_gemm(args), *a = &resolved;
-    int rc = validate_gemm(a);
-    if (rc) return rc;
-    if (!a->A || !a->B || !a->C) return unsupported("null A, B or C");
-    if (!aligned(a->A, 16) || !aligned(a->B, 16) || !aligned(a->C, 16))
-      return unsupported("A, B and C must be 16-byte aligned");
-    if ((a->scale_a && !aligned(a->scale_a, 16)) || (a->scale_b && !aligned(a->scale_b, 16)))
-      return unsupported("scales must be 16-byte aligned");
-    const TileDesc* t = tile_desc(a->tile_id);
-    if (a->scale_mode == SKG_SCALE_MX_E8M0 && (!a->scale_a || !a->scale_b))
-      return unsupported("MX block scales need both scale arrays");
-    GemmInst inst = gemm_instance(a->tile_id, a->dtype_ab, a->scale_mode);
-    if (!inst.launch) return unsupported("no GEMM instance for this tile and dtype");
-    int cus = 0, per_cu = 0;
-    rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu);
-    if (rc) return rc;
-    skg_plan_t pl;
-    rc = plan_launch(gemm_shape(a, *t), *t, a->mode, a->reduction, a->ctas,
-                     resolve_sk_order(a->sk_order, false), cus, per_cu, &pl);
-    if (rc) return rc;
-    rc = check_run(pl, ws, ws_bytes, cus, per_cu);
-    if (rc) return rc;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->dtype_ab == SKG_F4E2M1 && pl.reduction != SKG_RED_ATOMIC) {
-      // Kernel resets, so that the call may be captured into a graph.
-      const size_t bytes = !pl.sk_ctas ? 0 : (size_t)(handoff_reduction(pl.reduction) ? pl.flags_bytes : pl.workspace_bytes);
-      hipError_t e = zero_fill(ws, bytes, st);
-      if (e != hipSuccess) return hip_failure(std::string("reset: ") + hipGetErrorString(e));
-    } else {
-      rc = reset_scratch(pl, ws, st);
-      if (rc) return rc;
-    }
-    if (pl.reduction == SKG_RED_ATOMIC && pl.sk_ctas) {
-      hipError_t e = hipMemset2DAsync(a->C, (size_t)a->ldc * 4, 0, (size_t)a->N * 4, (size_t)a->M, st);
-      if (e != hipSuccess) return hip_failure(std::string("zeroing C: ") + hipGetErrorString(e));
-    }
-    GemmParams g;
-    g.A = static_cast<const char*>(a->A);
-    g.B = static_cast<const char*>(a->B);
-    g.C = static_cast<char*>(a->C);
-    g.M = (int)a->M;
-    g.N = (int)a->N;
-    g.K = (int)a->K;
-    g.lda_b = (uint32_t)row_bytes(a->dtype_ab, a->lda);
-    g.ldb_b = (uint32_t)row_bytes(a->dtype_ab, a->ldb);
-    g.ldc = (int)a->ldc;
-    g.sa = a->scale_a;
-    g.sb = a->scale_b;
-    g.dtype_c = a->dtype_c == SKG_F32 ? DT_F32 : (a->dtype_c == SKG_F16 ? DT_F16 : DT_BF16);
-    const int inject = injected_fault();
-    if (inject == INJECT_LAUNCH) return hip_failure("launch: failure injected by SKG_FAULT=launch");
-    hipError_t e = inst.launch(g, to_kplan(pl, inject, cus), carve(pl, ws), st, g_ev_start, g_ev_stop);
-    if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
-    return SKG_OK;
+    return run_gemm(args, ws, ws_bytes, stream, nullptr, nullptr);
+  } catch (const std::exception& ex) {
+    return hip_failure(std::string("exception: ") + ex.what());
+  } catch (...) {
+    return hip_failure("unknown exception");
+  }
+}
+
+int skg_plan_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream, skg_plan_t* plan,
+                      int32_t* launched) {
+  try {
+    clear_error();
+    if (!plan || !launched) return unsupported("null output");
+    *launched = 0;
+    return run_gemm(args, ws, ws_bytes, stream, plan, launched);
   } catch (const std::exception& ex) {
     return hip_failure(std::string("exception: ") + ex.what());
   } catch (...) {

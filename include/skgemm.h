@@ -434,6 +434,11 @@ int skg_wgrad_workspace_bytes(const skg_wgrad_args_t* args, size_t* out);
  * a pool larger than the device's resident capacity for the instance is
  * rejected with -2.  stream is a hipStream_t (NULL: the null stream). */
 int skg_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream);
+/* skg_plan_gemm and skg_run_gemm in one: fills *plan and runs it if ws_bytes
+ * is enough for it (*launched 1), so that a call whose plan takes no workspace
+ * is planned once.  Otherwise nothing is enqueued (*launched 0, status 0). */
+int skg_plan_run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream,
+                      skg_plan_t* plan, int32_t* launched);
 int skg_run_wgrad(const skg_wgrad_args_t* args, void* ws, size_t ws_bytes, void* stream);
 int skg_run_fwd(const skg_conv_args_t* args, void* ws, size_t ws_bytes, void* stream);
 int skg_run_dgrad(const skg_conv_args_t* args, void* ws, size_t ws_bytes, void* stream);

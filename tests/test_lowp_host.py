@@ -196,3 +196,11 @@ def test_auto_tile():
     assert (p["tm"], p["tn"]) == (256, 256) and p["mode"] == skg.MODES["dp"]
     p = plan(M=48, N=4864, K=4096, tile="auto", mode="dp_sk", reduction="tree", ctas=64)()
     assert p["tm"] >= 128 and p["sk_ctas"] == 64
+
+
+def test_plan_and_run_in_one_refuses_as_the_two_do():
+    a = skg.gemm_args(None, P, P, M=8, N=8, K=128, dtype_ab="e2m1", dtype_c="bf16", scale_a=P, scale_b=P,
+                      scale_mode="mx", tile="auto", mode="auto", reduction="auto", ctas=1)
+    refused(lambda: skg.skg_plan_run_gemm(a, 0, 0, 0), "null A, B or C")
+    a.A, a.K = P.data_ptr(), 100
+    refused(lambda: skg.skg_plan_run_gemm(a, 0, 0, 0), "multiple of 128")
