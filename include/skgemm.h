@@ -93,7 +93,7 @@ enum skg_scale_mode {
    *                    C[m][n] = round(sum_b 2^(sa[m][b]-127) 2^(sb[n][b]-127)
    *                    sum_{k in b} a(m,k) b(k,n)).  fp8 / bf8 inputs with
    *                    the 128x128x128 or 256x256x128 tile, or fp4 inputs
-   *                    with a 256-deep one; K a multiple of 128, both
+   *                    with one of the fp4 tiles; K a multiple of 128, both
    *                    pointers non-NULL and 16-byte aligned; no further
    *                    scale. */
   SKG_SCALE_MX_E8M0 = 2
@@ -205,8 +205,8 @@ enum skg_sk_order {
 /* Compiled tile instances.  TM x TN x TK in elements; each instance exists
  * for the operations and input types skg_tile_info reports. */
 enum skg_tile {
-  /* fp4 GEMM only: the call picks the tile from M, N and K (the plan's tm, tn
-     and tk report it). */
+  /* fp4 GEMM only: the call picks the tile from M, N, K and the mode (the
+     plan's tm, tn and tk report it). */
   SKG_TILE_AUTO = -1,
   SKG_TILE_128x128x32 = 0,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x256x64 = 1,   /* f16/bf16 GEMM and wgrad, 4 waves */
@@ -224,8 +224,10 @@ enum skg_tile {
                                 of 16 input and 16 output channels (GEMM-N =
                                 64 channels), two filter taps per MAC
                                 iteration, 4 waves */
-  SKG_TILE_256x256x256 = 9,  /* fp4 GEMM with MX block scales, 4 waves */
-  SKG_TILE_128x128x256 = 10, /* fp4 GEMM with MX block scales, 4 waves */
+  /* fp4 GEMM with MX block scales, 4 waves.  Mode auto is dp, which takes no
+     workspace and walks the plan's grid with at most one workgroup a CU. */
+  SKG_TILE_256x256x256 = 9,
+  SKG_TILE_128x128x256 = 10,
   /* fp4 GEMM with MX block scales, for few tiles: 4 waves that split the
      reduction; mode dp or auto, no workspace */
   SKG_TILE_16x16x512 = 11,
