@@ -21,8 +21,9 @@ TILE_AUTO = -1
 TILE_128x128x32, TILE_256x256x64, TILE_256x256x128, TILE_32x64x64, TILE_128x128x64, \
     TILE_256x128x64, TILE_128x128x128, TILE_64x144x32, TILE_128x64x32, TILE_256x256x256, \
     TILE_128x128x256, TILE_16x16x512, TILE_16x32x512, \
-    TILE_16x64x512, TILE_32x32x512, TILE_32x64x512, TILE_48x32x512, TILE_64x64x512 = range(18)
-TILE_COUNT = 18
+    TILE_16x64x512, TILE_32x32x512, TILE_32x64x512, TILE_48x32x512, TILE_64x64x512, \
+    TILE_256x128x256 = range(19)
+TILE_COUNT = 19
 
 MODES = {"dp": MODE_DP, "dp_sk": MODE_DP_SK, "persistent": MODE_PERSISTENT,
          "splitk": MODE_SPLITK, "auto": MODE_AUTO}
@@ -42,7 +43,7 @@ TILES = {"128x128x32": TILE_128x128x32, "256x256x64": TILE_256x256x64,
          "128x128x256": TILE_128x128x256, "16x16x512": TILE_16x16x512, "16x32x512": TILE_16x32x512,
          "16x64x512": TILE_16x64x512, "32x32x512": TILE_32x32x512,
          "32x64x512": TILE_32x64x512, "48x32x512": TILE_48x32x512,
-         "64x64x512": TILE_64x64x512}
+         "64x64x512": TILE_64x64x512, "256x128x256": TILE_256x128x256}
 
 
 class skg_tile_info_t(ctypes.Structure):

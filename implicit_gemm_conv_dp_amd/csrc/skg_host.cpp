@@ -45,6 +45,7 @@ const TileDesc kTiles[SKG_TILE_COUNT] = {
     /* 32x64x512 */ {32, 64, 512, 4, M_F4, 0, 0, 0, true},
     /* 48x32x512 */ {48, 32, 512, 4, M_F4, 0, 0, 0, true},
     /* 64x64x512 */ {64, 64, 512, 4, M_F4, 0, 0, 0, true},
+    /* 256x128x256 */ {256, 128, 256, 4, M_F4, 0, 0, 0, true},
 };
 
 // Offsets inside one buffer are 32-bit on the device (buffer resources).
@@ -154,8 +155,8 @@ int plan_launch(const GemmShape& g, const TileDesc& t, int mode, int reduction, 
                 int sk_order, int num_cus, int resident_per_cu, skg_plan_t* out) {
   const int requested = mode;
   int slices = 1;
-  if (t.direct && mode != SKG_MODE_AUTO && mode != SKG_MODE_DP)
-    return unsupported("this tile splits K within its workgroup: mode dp or auto");
+  if (t.dp_only && mode != SKG_MODE_AUTO && mode != SKG_MODE_DP)
+    return unsupported("this tile runs whole tiles a workgroup: mode dp or auto");
   // fp4: the dp kernels are ahead of every split over the whole sweep of
   // resolve_gemm (1500x1500x4096 15.9 us against 30.3 on stream-K).
   if ((t.gemm_mask & M_F4) && mode == SKG_MODE_AUTO) mode = SKG_MODE_DP;
@@ -332,7 +333,8 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
 
 // The fp4 tile of a call that leaves it open: the least of the times that these
 // models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
-// 8192, K 256 to 8192) on all tiles, most within 15 % of the measured.
+// 8192, K 256 to 8192) on all tiles.  On 73 others drawn over these ranges the
+// tile it picks takes 1.5 % longer than the best one, on average.
 // - A direct tile's workgroups take their operands' rows in at 60 kB/us a CU,
 //   the larger ones after a start that nothing covers (one workgroup a CU),
 //   and short reductions cost a round of workgroups its latency:
@@ -341,7 +343,9 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
 //   (19.3 on 128x128, 19.5 on 32x32).
 // - A ring tile costs a start and end and its iterations, a workgroup a CU at
 //   a time: 512x8192x1024 9.2 us on 128x128 (20.0 on direct 64x64, 15.2 on
-//   256x256), 4096x4096x1024 22.2 on 256x256 (25.9 on 128x128).
+//   256x256), 4096x4096x4096 39.9 on 256x256 (45.6 on 256x128, 50.4 on
+//   128x128), 7349x2145x4224 52.2 on 256x128 (56.9 on 128x128, 73.7 on
+//   256x256).
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   skg_gemm_args_t r = *a;
   if (r.tile_id != SKG_TILE_AUTO || r.dtype_ab != SKG_F4E2M1) return r;
@@ -351,17 +355,17 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   double best = 1e300;
   for (int id = 0; id < SKG_TILE_COUNT; ++id) {
     const TileDesc& t = kTiles[id];
-    if (!(t.gemm_mask & M_F4) || (t.direct && !dp)) continue;
+    if (!(t.gemm_mask & M_F4) || (t.dp_only && !dp)) continue;
     const double rounds = (double)ceil_div(ceil_div(r.M, t.tm) * ceil_div(r.N, t.tn), 256);  // CUs of a gfx950
     double us;
-    if (t.direct) {
+    if (t.tk == 512) {
       const int64_t rows = std::min<int64_t>(t.tm, r.M) + std::min<int64_t>(t.tn, r.N);
       const double bytes = (double)rows * (double)r.K * (0.5 + 1.0 / 32);
-      const double start = std::max(0, t.tm + t.tn - 64) * 0.036, least = (t.tm + t.tn - 18) * 0.04;
+      const double start = std::max(0, t.tm + t.tn - 60) * 0.036, least = (t.tm + t.tn - 18) * 0.04;
       us = 1.6 + rounds * std::max(bytes / 60e3 + start, least);
     } else {
       const double iters = (double)ceil_div(r.K, t.tk);
-      us = rounds * (t.tm == 256 ? 12 + 1.5 * iters : 5 + 0.45 * iters);
+      us = rounds * (t.tn == 256 ? 12 + 1.5 * iters : t.tm == 256 ? 8 + 0.9 * iters : 5.4 + 0.43 * iters);
     }
     if (us < best) {
       best = us;
@@ -383,7 +387,7 @@ int validate_gemm(const skg_gemm_args_t* a) {
     return unsupported("unknown scale mode");
   if (a->scale_mode == SKG_SCALE_MX_E8M0) {
     if (a->dtype_ab == SKG_F4E2M1) {
-      if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need the 256x256x256, 128x128x256 or a 512-deep tile");
+      if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need an fp4 tile");
     } else {
       if (a->dtype_ab != SKG_F8E4M3 && a->dtype_ab != SKG_F8E5M2)
         return unsupported("MX block scales need fp8, bf8 or fp4 inputs");

@@ -27,7 +27,7 @@ struct TileDesc {
   int wgrad_mask;  // 1 << skg_dtype accepted as wgrad X/dY
   int conv_mask;   // 1 << skg_dtype accepted for forward conv / dgrad
   int group_block; // block-diagonal wgrad tile: whole 16-channel groups per tile (0: dense)
-  bool direct = false;  // one workgroup a tile, its waves split K: no stream-K modes
+  bool dp_only = false;  // no stream-K modes
 };
 
 const TileDesc* tile_desc(int tile_id);

@@ -237,7 +237,8 @@ enum skg_tile {
   SKG_TILE_32x64x512 = 15,
   SKG_TILE_48x32x512 = 16,
   SKG_TILE_64x64x512 = 17,
-  SKG_TILE_COUNT = 18
+  SKG_TILE_256x128x256 = 18, /* fp4 GEMM with MX block scales, 4 waves; mode dp or auto */
+  SKG_TILE_COUNT = 19
 };
 
 enum skg_op { SKG_OP_GEMM = 0, SKG_OP_WGRAD = 1, SKG_OP_FWD = 2, SKG_OP_DGRAD = 3 };

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 T = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 TILES = ["16x16x512", "16x32x512", "16x64x512", "32x32x512", "32x64x512", "48x32x512", "64x64x512",
-         "128x128x256", "256x256x256"]
+         "128x128x256", "256x256x256", "256x128x256"]
 
 
 def operand(seed, rows, K):
@@ -93,7 +93,7 @@ def test_not_a_number_stays_in_its_row(tile):
 
 
 @pytest.mark.parametrize("tile,dtype_c", [("128x128x256", "bf16"), ("128x128x256", "f32"), ("256x256x256", "f16"),
-                                          ("256x256x256", "f32"), ("64x64x512", "bf16")])
+                                          ("256x256x256", "f32"), ("256x128x256", "bf16"), ("64x64x512", "bf16")])
 def test_more_tiles_than_workgroups(tile, dtype_c):
     """Workgroups that take a second and a third tile, with the last strips of
     tiles cut short, for reductions of one, two and five iterations."""

@@ -170,9 +170,9 @@ def test_fp4_plan():
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(tile="16x16x512", mode="dp_sk", reduction="tree"), "splits K"),
-    (dict(tile="64x64x512", mode="splitk", reduction="linear"), "splits K"),
-    (dict(tile="32x32x512", mode="persistent"), "splits K"),
+    (dict(tile="16x16x512", mode="dp_sk", reduction="tree"), "mode dp or auto"),
+    (dict(tile="64x64x512", mode="splitk", reduction="linear"), "mode dp or auto"),
+    (dict(tile="32x32x512", mode="persistent"), "mode dp or auto"),
     (dict(tile="16x16x512", scale_mode="rowcol"), "MX"),
 ])
 def test_direct_tile_refusals(kw, word):
