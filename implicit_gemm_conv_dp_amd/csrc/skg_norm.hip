@@ -298,7 +298,7 @@ struct NormBwdParams {
   const char *dy, *h, *w, *dres;
   const float* rstd;
   char* dx;
-  float* partial;  // [workgroups][cols], or nullptr without dw
+  float* partial;  // [workgroups][cols] (few rows: dw itself), or nullptr without dw
   int rows, cols, w_f32;
   int64_t lddy, ldh, ldr, lddx;
   float inv_cols;
@@ -398,6 +398,104 @@ __global__ __launch_bounds__(S::THREADS) void rmsnorm_bwd_kernel(NormBwdParams p
   norm_bwd_rows<DT, S, 1>(p, (SKG_LDS float*)lds);
 }
 
+// Few rows, both gradients at once: the first workgroups take the rows (dx), the
+// others 32 columns each (dw), which read dy and h again, from the cache.
+// One launch and no workspace instead of two and one.
+constexpr int kSmallThreads = 1024, kRuns = 32, kSmallCols = 16384;
+
+template <int DT, class S, int TAIL>
+SKG_DEV void norm_bwd_row(const NormBwdParams& p, SKG_LDS uint32_t* slots) {
+  typedef typename Elem<DT>::raw raw;
+  constexpr int NCH = S::NCH, G = S::SIZE, GROUPS = kSmallThreads / G;
+  const int t = threadIdx.x % G, grp = threadIdx.x / G, at = blockIdx.x * GROUPS + grp;
+  const int row = min(at, p.rows - 1);
+  Chunk<DT> dy[NCH], h[NCH], r[NCH];
+  load_row<DT, S, TAIL>(dy, p.dy, row, p.lddy, t, p.cols);
+  load_row<DT, S, TAIL>(h, p.h, row, p.ldh, t, p.cols);
+  if (p.dres) load_row<DT, S, TAIL>(r, p.dres, row, p.ldr, t, p.cols);
+  const float s = p.rstd[row];
+  float w[NCH][8];
+  load_weights<DT, S, TAIL>(w, p.w, p.w_f32, t, p.cols);
+  place_row<DT, S, TAIL>(dy, t, p.cols);
+  place_row<DT, S, TAIL>(h, t, p.cols);
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part = __builtin_fmaf(dy[i].get(j) * w[i][j], h[i].get(j) * s, part);
+    dot += part;
+  }
+  dot = lanes_reduce<OpSum, S::LANES>(dot);
+  if constexpr (S::WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = __builtin_bit_cast(uint32_t, dot);
+    __syncthreads();
+    dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::WAVES; ++k) dot += __builtin_bit_cast(float, (uint32_t)slots[grp * S::WAVES + k]);
+  }
+  dot *= p.inv_cols;
+  if (at >= p.rows) return;
+  if (p.dres) place_row<DT, S, TAIL>(r, t, p.cols);
+  raw* dx = reinterpret_cast<raw*>(p.dx) + row * p.lddx;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int left = p.cols - (t + i * G) * 8;
+    Chunk<DT> c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = s * __builtin_fmaf(-h[i].get(j) * s, dot, dy[i].get(j) * w[i][j]);
+      c.put(j, p.dres ? v + r[i].get(j) : v);
+    }
+    if (left > 0) store_chunk<DT>(dx + (t + i * G) * 8, TAIL ? left : 8, c);
+  }
+}
+
+// Thread (run, column) adds rows run, run + 32, ..., eight at a time in flight;
+// then the runs, in order.
+template <int DT>
+SKG_DEV void norm_dw_columns(const NormBwdParams& p, int block, SKG_LDS float* part) {
+  typedef typename Elem<DT>::raw raw;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c0 = block * 32 + lane, c = min(c0, p.cols - 1);
+  const raw* dy = reinterpret_cast<const raw*>(p.dy) + c;
+  const raw* h = reinterpret_cast<const raw*>(p.h) + c;
+  float sum = 0.f;
+  for (int row = run; row < p.rows; row += 8 * kRuns) {
+    raw a[8], b[8];
+    float s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t r = min(row + k * kRuns, p.rows - 1);
+      a[k] = dy[r * p.lddy];
+      b[k] = h[r * p.ldh];
+      s[k] = p.rstd[r];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      sum = row + k * kRuns < p.rows ? __builtin_fmaf(Elem<DT>::get(a[k]), Elem<DT>::get(b[k]) * s[k], sum) : sum;
+  }
+  part[run * 33 + lane] = sum;
+  __syncthreads();
+  if (run == 0 && c0 < p.cols) {
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) total += part[k * 33 + lane];
+    p.partial[c0] = total;
+  }
+}
+
+template <int DT, class S>
+__global__ __launch_bounds__(kSmallThreads) void rmsnorm_bwd_small_kernel(NormBwdParams p, int row_blocks) {
+  __shared__ float lds[kRuns * 33];
+  if ((int)blockIdx.x >= row_blocks) return norm_dw_columns<DT>(p, blockIdx.x - row_blocks, (SKG_LDS float*)lds);
+  SKG_LDS uint32_t* slots = (SKG_LDS uint32_t*)(SKG_LDS float*)lds;
+  if (!(p.cols & 7)) return norm_bwd_row<DT, S, 0>(p, slots);
+  if constexpr (S::COLS == kSmallSpread) {
+    if (p.cols < 8) return norm_bwd_row<DT, S, 2>(p, slots);
+  }
+  norm_bwd_row<DT, S, 1>(p, slots);
+}
+
 // dw[c] = sum of the groups' partial[g][c], in a fixed order: 32 columns by 32
 // runs of groups a workgroup, then the runs.  A run's loads are in flight
 // together, so the time is a few latencies however many groups there are
@@ -457,9 +555,17 @@ void launch_norm(const NormParams& p, int out, hipStream_t st) {
   with_spread(p.cols, [&](auto s) { launch_norm<DT, decltype(s)>(p, out, st); });
 }
 template <int DT>
-void launch_norm_bwd(const NormBwdParams& p, int groups, hipStream_t st) {
+void launch_norm_bwd(const NormBwdParams& p, int groups, bool small, hipStream_t st) {
   with_spread(p.cols, [&](auto s) {
     typedef decltype(s) S;
+    if constexpr (S::COLS <= kSmallCols) {
+      if (small) {
+        const int rows = p.dx ? (int)ceil_div(p.rows, kSmallThreads / S::SIZE) : 0;
+        hipLaunchKernelGGL((rmsnorm_bwd_small_kernel<DT, S>), dim3((unsigned)(rows + ceil_div(p.cols, 32))),
+                           dim3(kSmallThreads), 0, st, p, rows);
+        return;
+      }
+    }
     hipLaunchKernelGGL((rmsnorm_bwd_kernel<DT, S>), dim3((unsigned)groups), dim3(S::THREADS), 0, st, p);
   });
 }
@@ -544,6 +650,23 @@ int check_norm_bwd(const skg_norm_bwd_args_t* a) {
   return SKG_OK;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+// Whether both gradients come from one launch without a workspace.  The
+// columns' share reads dy and h a second time, which is cheaper than a second
+// launch and the partial sums (509x1111 f32 5.9 us a call against 9.2,
+// 1000x1024 bf16 7.1 against 9.7; even at 1024x4096).  Not where dx is written
+// over what that share reads; and larger calls give dw the same bits whether
+// or not it is.
+bool bwd_small(const skg_norm_bwd_args_t* a) {
+  if (!a->dw || a->rows < 1 || a->rows > 1024 || a->cols > kSmallCols || a->rows * a->cols > 1 << 20) return false;
+  if (!a->dx) return true;
+  const size_t es = elem_bytes(a->dtype);
+  auto bytes = [&](int64_t ld) { return ((a->rows - 1) * ld + a->cols) * es; };
+  return !overlap(a->dx, bytes(a->lddx), a->dy, bytes(a->lddy)) && !overlap(a->dx, bytes(a->lddx), a->h, bytes(a->ldh));
+}
 // Workgroups, each with one row of partial dw sums.
 int bwd_groups(const skg_norm_bwd_args_t* a) {
   int64_t groups = 0;
@@ -566,7 +689,8 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
       !aligned_to(a->weight, elem_bytes(a->dtype_w)) || !aligned_to(a->rstd, 4) || !aligned_to(a->dw, 4))
     return unsupported("pointers must be aligned to their elements");
   const int groups = bwd_groups(a);
-  const size_t need = a->dw ? size_t(groups) * a->cols * 4 : 0;
+  const bool small = bwd_small(a);
+  const size_t need = a->dw && !small ? size_t(groups) * a->cols * 4 : 0;
   if (need > ws_bytes) return unsupported("workspace too small for this call");
   if (need && (!ws || !aligned_to(ws, 16))) return unsupported("workspace must be 16-byte aligned device memory");
   int cus = 0;
@@ -581,7 +705,7 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
     p.dres = static_cast<const char*>(a->dres);
     p.rstd = a->rstd;
     p.dx = static_cast<char*>(a->dx);
-    p.partial = a->dw ? static_cast<float*>(ws) : nullptr;
+    p.partial = small ? a->dw : a->dw ? static_cast<float*>(ws) : nullptr;
     p.rows = (int)a->rows;
     p.cols = (int)a->cols;
     p.w_f32 = a->dtype_w == SKG_F32;
@@ -591,15 +715,15 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
     p.lddx = a->lddx;
     p.inv_cols = 1.f / (float)a->cols;
       if (a->dtype == SKG_F16)
-      launch_norm_bwd<DT_F16>(p, groups, st);
+      launch_norm_bwd<DT_F16>(p, groups, small, st);
     else if (a->dtype == SKG_BF16)
-      launch_norm_bwd<DT_BF16>(p, groups, st);
+      launch_norm_bwd<DT_BF16>(p, groups, small, st);
     else
-      launch_norm_bwd<DT_F32>(p, groups, st);
+      launch_norm_bwd<DT_F32>(p, groups, small, st);
     e = hipGetLastError();
     if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   }
-  if (a->dw) {
+  if (a->dw && !small) {
     hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)ceil_div(a->cols, 32)), dim3(1024), 0, st,
                        static_cast<const float*>(ws), a->dw, groups, (int)a->cols);
     e = hipGetLastError();
@@ -632,7 +756,7 @@ int skg_rmsnorm_bwd_workspace_bytes(const skg_norm_bwd_args_t* a, size_t* out) {
     const int rc = check_norm_bwd(a);
     if (rc) return rc;
     if (!out) return unsupported("null output");
-    *out = a->dw ? size_t(bwd_groups(a)) * a->cols * 4 : 0;
+    *out = a->dw && !bwd_small(a) ? size_t(bwd_groups(a)) * a->cols * 4 : 0;
     return SKG_OK;
   } catch (...) {
     return hip_failure("exception in skg_rmsnorm_bwd_workspace_bytes");

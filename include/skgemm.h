@@ -532,7 +532,8 @@ typedef struct skg_norm_args {
  *        residual alike; dres, or NULL, is what reaches h from above);
  *   dw = sum over rows of dy * h * s        fp32, in a fixed order.
  * A quantised y passes its gradient through unchanged.  dx (which may be dy
- * or dres) or dw may be NULL.  The workspace holds partial sums of dw. */
+ * or dres) or dw may be NULL.  The workspace holds partial sums of dw; few
+ * rows take none. */
 typedef struct skg_norm_bwd_args {
   int64_t rows, cols;
   int32_t dtype;           /* dy, h, dres, dx */

@@ -137,3 +137,38 @@ def test_many_chunks_with_ragged_lines(fmt):
     assert np.array_equal(got, lowp.decode(fmt, rq))
     want = torch.from_numpy(lowp.mx_values(rs, rq, fmt)[:, :cols]).float().to(torch.bfloat16)
     assert torch.equal(back[:, :cols].cpu(), want) and torch.isnan(back[:, cols:].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 5), (31, 274), (33, 8), (509, 1111), (1024, 1024), (1025, 300), (257, 4079),
+                                       (64, 16384), (65, 16384), (700, 33)])
+def test_gradients_of_few_rows(rows, cols, dtype):
+    """Both sides of the size up to which one launch makes both gradients: the
+    values, and the same bits whichever are asked for and wherever dx goes."""
+    h, dy, dres = (rows_of(s, rows, cols, dtype) for s in (10, 11, 12))
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    kw = dict(rows=rows, cols=cols, dtype=dtype)
+    dx, dw, alone = out((rows, cols), T[dtype]), out((cols,), torch.float32), out((cols,), torch.float32)
+    skg.rmsnorm_bwd(dy, h, rstd, dx, dres=dres, dw=dw, **kw)
+    skg.rmsnorm_bwd(dy, h, rstd, None, dw=alone, **kw)
+    only = out((rows, cols), T[dtype])
+    skg.rmsnorm_bwd(dy, h, rstd, only, dres=dres, **kw)
+    over_res, over_dy, dw2, dw3 = dres.clone(), dy.clone(), torch.empty_like(dw), torch.empty_like(dw)
+    skg.rmsnorm_bwd(dy, h, rstd, over_res, dres=over_res, dw=dw2, **kw)
+    skg.rmsnorm_bwd(over_dy, h, rstd, over_dy, dres=dres, dw=dw3, **kw)
+    torch.cuda.synchronize()
+    for t in (only, over_res, over_dy):
+        assert torch.equal(t, dx)
+    assert torch.equal(alone, dw) and torch.equal(dw2, dw)
+    H, DY, S, R = (f64(t) for t in (h, dy, rstd, dres))
+    rx, rw = lowp.rmsnorm_bwd(DY, H, S, np.ones(cols))
+    rx = rx + R
+    u = 2.0 ** -24
+    n = H * S[:, None]
+    # as in the gradient's tests at other sizes
+    tol = S[:, None] * (8 * u * np.abs(DY) + np.abs(n) * 80 * u * np.mean(np.abs(DY * n), 1, keepdims=True))
+    tiny = float(torch.finfo(T[dtype]).smallest_normal) * HALF[dtype] * 2
+    tol = tol + 8 * u * np.abs(R) + HALF[dtype] * np.abs(rx) * (1 + 2.0 ** -10) + tiny
+    assert np.all(np.abs(f64(dx) - rx) <= tol)
+    for t in (dw, dw3):
+        assert np.all(np.abs(f64(t) - rw) <= (rows + 4) * u * np.sum(np.abs(DY * n), 0) + 2.0 ** -126)
