@@ -23,19 +23,19 @@ tile="auto")`` for their product.
 from . import _lib
 from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  # noqa: F401
                    skg_plan_run_gemm, skg_plan_wgrad, skg_profile_events, skg_run_gemm,
-                   skg_run_wgrad,
-                   skg_tile_info, skg_gemm_workspace_bytes, skg_wgrad_workspace_bytes,
+                   skg_run_wgrad, skg_tile_info, skg_gemm_workspace_bytes, skg_wgrad_workspace_bytes,
                    skg_fixup_timeouts, skg_run_wgrad_static, skg_plan_fwd, skg_plan_dgrad,
                    skg_run_fwd, skg_run_dgrad, skg_run_rmsnorm, skg_run_rmsnorm_bwd,
-                   skg_rmsnorm_bwd_workspace_bytes, skg_run_mx_quant, skg_run_mx_dequant, MODES, REDUCTIONS, DTYPES, TILES, SCALE_MODES,
-                   SK_ORDERS)
+                   skg_rmsnorm_bwd_workspace_bytes, skg_run_mx_quant, skg_run_mx_dequant, MODES,
+                   REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS)
 
 __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd", "plan_dgrad",
            "gemm_args", "wgrad_args", "conv_args",
            "workspace_for", "SkgError", "MODES", "REDUCTIONS", "DTYPES", "TILES", "SCALE_MODES",
            "SK_ORDERS",
            "skg_default_pool", "skg_device_info", "skg_plan_gemm", "skg_plan_wgrad",
-           "skg_run_gemm", "skg_plan_run_gemm", "skg_run_wgrad", "skg_tile_info", "skg_profile_events",
+           "skg_run_gemm", "skg_plan_run_gemm", "skg_run_wgrad", "skg_tile_info",
+           "skg_profile_events",
            "skg_gemm_workspace_bytes", "skg_wgrad_workspace_bytes", "skg_fixup_timeouts",
            "skg_run_wgrad_static", "skg_plan_fwd", "skg_plan_dgrad", "skg_run_fwd",
            "skg_run_dgrad", "rmsnorm", "rmsnorm_bwd", "mx_quant", "mx_dequant",
