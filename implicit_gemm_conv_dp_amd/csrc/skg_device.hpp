@@ -59,8 +59,10 @@ SKG_DEV i32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
 // wait before every later LDS read would serialise the pipeline, and the
 // engine orders these loads with explicit vmcnt waits and barriers instead.
 // (Loads the compiler cannot see only make its own vmcnt waits stricter.)
+// The s_nop is the wait state that has to pass between a scalar write of M0
+// and such a load; the compiler inserts none inside a statement.
 SKG_DEV void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds_base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
                :
                : "v"(voff), "s"(lds_base), "s"(r)
                : "memory", "m0");
@@ -69,7 +71,7 @@ SKG_DEV void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds_base, uint32_t voff) {
 // 4 bytes per lane straight into LDS (lane i at lds_base + 4*i); ordered
 // like dma16, by the engine's own vmcnt waits.
 SKG_DEV void dma4(__amdgpu_buffer_rsrc_t r, uint32_t lds_base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %0, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, 0 offen lds"
                :
                : "v"(voff), "s"(lds_base), "s"(r)
                : "memory", "m0");

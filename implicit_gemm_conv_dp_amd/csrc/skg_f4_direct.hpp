@@ -71,7 +71,7 @@ struct F4Direct {
   // Row DMA n of the operand into a slot's part; kb: byte offset along K.
   template <int N>
   SKG_DEV static void dma_rows(const Operand& o, uint32_t dst, uint32_t kb) {
-    asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(dst), "v"(o.off[N & 1] + N * o.pitch8), "s"(o.rows), "s"(kb), "n"(N * 1024)
                  : "memory", "m0", "scc");

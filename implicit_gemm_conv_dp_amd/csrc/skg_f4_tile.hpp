@@ -133,7 +133,7 @@ struct F4Tile {
   // 16 bytes a lane to LDS address dst + IMM, from a scalar offset along the rows.
   template <int IMM>
   SKG_DEV static void dma_row(const i32x4& r, uint32_t dst, uint32_t voff, uint32_t kb) {
-    asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(dst), "v"(voff), "s"(r), "s"(kb), "n"(IMM)
                  : "memory", "m0", "scc");
