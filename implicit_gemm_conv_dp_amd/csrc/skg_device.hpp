@@ -60,11 +60,15 @@ SKG_DEV i32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
 // engine orders these loads with explicit vmcnt waits and barriers instead.
 // (Loads the compiler cannot see only make its own vmcnt waits stricter.)
 // The s_nop is the wait state that has to pass between a scalar write of M0
-// and such a load; the compiler inserts none inside a statement.
+// and such a load; the compiler inserts none inside a statement.  Nor does it
+// before one: a resource that it has just read back from spilled scalar
+// registers (v_readlane) needs five wait states before the load uses it, the
+// write of M0 and NOPS + 1 more.  Loaders whose resources it spills ask for 3.
+template <int NOPS = 0>
 SKG_DEV void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds_base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop %3\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
                :
-               : "v"(voff), "s"(lds_base), "s"(r)
+               : "v"(voff), "s"(lds_base), "s"(r), "n"(NOPS)
                : "memory", "m0");
 }
 

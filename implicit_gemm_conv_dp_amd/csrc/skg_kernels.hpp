@@ -1010,9 +1010,9 @@ struct WgradBdLoader {
   // tap planes.
   SKG_DEV void issue_iter(int it, SKG_LDS char* e) const {
     const QBase b = qbase(it);
-    dma16(rdy, lds_addr(e + wave * 1024), a_off(b));
+    dma16<3>(rdy, lds_addr(e + wave * 1024), a_off(b));
 #pragma unroll
-    for (int j = 0; j < TAPS; ++j) dma16(rx, lds_addr(e + (1 + j) * PLANE + wave * 1024), b_off(b, j));
+    for (int j = 0; j < TAPS; ++j) dma16<3>(rx, lds_addr(e + (1 + j) * PLANE + wave * 1024), b_off(b, j));
   }
 };
 

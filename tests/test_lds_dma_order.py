@@ -1,7 +1,9 @@
-"""M0 and the direct-to-LDS loads in the built code object (no GPU): such a
-load takes its LDS address from M0, and between a scalar write of M0 and the
-load one wait state has to pass.  The compiler puts it after its own writes;
-inside an asm statement the statement itself has to."""
+"""Wait states before the direct-to-LDS loads in the built code object (no
+GPU).  Such a load takes its LDS address from M0: one wait state has to pass
+between a scalar write of M0 and the load.  And five between a vector
+instruction that writes a scalar register (v_readlane, v_readfirstlane) and a
+memory instruction that reads it.  The compiler sees to both for its own
+loads; for those in asm statements the source has to."""
 
 import os
 import re
@@ -15,20 +17,49 @@ from test_host_library import code_objects, instrs, kernels
 WRITES_M0 = re.compile(r"^\w+ m0[, ]")
 
 
-def test_a_wait_state_between_m0_and_the_load():
+@pytest.fixture(scope="module")
+def loads():
+    """(kernel, the instructions up to and with the load) of every load."""
     if not os.path.exists(_lib.LIB_PATH):
         pytest.skip("library not built")
     with tempfile.TemporaryDirectory() as tmp:
         objs = code_objects(tmp)
-    loads, bad = 0, {}
+    found = []
     for dis in objs:
         for name, body in kernels(dis).items():
             ins = instrs(body)
-            for before, x in zip(ins, ins[1:]):
-                if x.startswith("buffer_load") and x.endswith(" lds"):
-                    loads += 1
-                    if WRITES_M0.match(before):
-                        bad[name] = bad.get(name, 0) + 1
-    assert loads, "no direct-to-LDS load in the library"
-    assert not bad, "%d of %d loads right after a write of M0, in %d kernels, such as %s" % (
-        sum(bad.values()), loads, len(bad), sorted(bad)[0])
+            found += [(name, ins[max(0, i - 6):i + 1]) for i, x in enumerate(ins)
+                      if x.startswith("buffer_load") and x.endswith(" lds")]
+    assert found, "no direct-to-LDS load in the library"
+    return found
+
+
+def test_a_wait_state_between_m0_and_the_load(loads):
+    bad = [name for name, ins in loads if WRITES_M0.match(ins[-2])]
+    assert not bad, "%d of %d loads right after a write of M0, such as in %s" % (len(bad), len(loads), bad[0])
+
+
+def scalars(operand):
+    m = re.match(r"s\[(\d+):(\d+)\]$", operand) or re.match(r"s(\d+)()$", operand)
+    return set(range(int(m[1]), int(m[2] or m[1]) + 1)) if m else set()
+
+
+def waited(ins):
+    """Wait states since a vector instruction wrote a scalar operand of the
+    last instruction: an instruction counts one, s_nop n counts n + 1."""
+    *before, load = [re.split(r"[ ,]+", x) for x in ins]
+    reads = set().union(*(scalars(o) for o in load[1:]))
+    states = 0
+    for op, *operands in reversed(before):
+        # (a carry or a scale is a second operand that is written)
+        written = operands[:2] if "_co_" in op or "div_scale" in op else operands[:1]
+        if op.startswith("v_") and any(scalars(o) & reads for o in written):
+            return states
+        states += int(operands[0]) + 1 if op == "s_nop" else 1
+    return 5
+
+
+def test_five_wait_states_after_vector_writes_of_scalars(loads):
+    assert waited(["v_readlane_b32 s11, v254, 36", "s_mov_b32 m0, s2", "s_nop 0", "buffer_load_dword v4, s[8:11], 0 offen lds"]) == 2
+    bad = [name for name, ins in loads if waited(ins) < 5]
+    assert not bad, "%d of %d loads, such as in %s" % (len(bad), len(loads), bad[0])
