@@ -20,6 +20,8 @@ e2m1 (4-bit) codes; and ``gemm(dtype_ab="e2m1", scale_mode="mx",
 tile="auto")`` for their product.
 """
 
+import contextlib
+
 from . import _lib
 from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  # noqa: F401
                    skg_plan_run_gemm, skg_plan_wgrad, skg_profile_events, skg_run_gemm,
@@ -169,12 +171,21 @@ def _handle(stream):
     return _current_handle()
 
 
+def _pool_of(stream):
+    """A context whose allocations come from the launch stream's pool: memory
+    of another stream's may have been freed there by work that is still to
+    run, which only that stream's own order makes safe."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
+
+
 def _run(run, args, plan, device, workspace, stream):
-    """One run call.  A workspace the call allocates itself is handed to the
-    caching allocator as used by the launch stream (record_stream), so its
-    memory is not given to another allocation before the kernel is done
-    with it, whichever stream the caller passed.  A plan without one allocates
-    nothing."""
+    """One run call.  A workspace the call allocates itself comes from the
+    launch stream's pool, so that whatever used its memory before and uses it
+    afterwards is ordered with the kernel, whichever stream the caller passed.
+    A plan without one allocates nothing."""
     if workspace is not None:
         run(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             _handle(stream))
@@ -182,7 +193,8 @@ def _run(run, args, plan, device, workspace, stream):
         run(args, 0, 0, _handle(stream))
     else:
         s = _launch_stream(stream)
-        ws = workspace_for(plan, device)
+        with _pool_of(stream):
+            ws = workspace_for(plan, device)
         ws.record_stream(s)
         run(args, ws.data_ptr(), ws.numel() * ws.element_size(), s.cuda_stream)
 
@@ -290,9 +302,8 @@ def rmsnorm_bwd(dy, h, rstd, dx, workspace=None, stream=None, **kw):
         need = skg_rmsnorm_bwd_workspace_bytes(args)
         if need:
             import torch
-            ws = torch.empty(need, dtype=torch.uint8, device=kw["dw"].device)
-            if stream is not None:
-                ws.record_stream(stream)
+            with _pool_of(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=kw["dw"].device)
     skg_run_rmsnorm_bwd(args, _ptr(ws), need, _handle(stream))
 
 
