@@ -62,14 +62,19 @@ SKG_DEV i32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
 // The s_nop is the wait state that has to pass between a scalar write of M0
 // and such a load; the compiler inserts none inside a statement.  Nor does it
 // before one: a resource that it has just read back from spilled scalar
-// registers (v_readlane) needs five wait states before the load uses it, the
-// write of M0 and NOPS + 1 more.  Loaders whose resources it spills ask for 3.
-template <int NOPS = 0>
+// registers (v_readlane) needs five wait states before the load uses it, so
+// loaders whose resources it spills have settle() between the two.
 SKG_DEV void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds_base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop %3\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
                :
-               : "v"(voff), "s"(lds_base), "s"(r), "n"(NOPS)
+               : "v"(voff), "s"(lds_base), "s"(r)
                : "memory", "m0");
+}
+
+// Has two resources in scalar registers, and what wrote them five wait states
+// in the past.
+SKG_DEV void settle(__amdgpu_buffer_rsrc_t& a, __amdgpu_buffer_rsrc_t& b) {
+  asm volatile("s_nop 4" : "+s"(a), "+s"(b));
 }
 
 // 4 bytes per lane straight into LDS (lane i at lds_base + 4*i); ordered

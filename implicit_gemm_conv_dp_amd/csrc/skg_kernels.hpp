@@ -1010,9 +1010,13 @@ struct WgradBdLoader {
   // tap planes.
   SKG_DEV void issue_iter(int it, SKG_LDS char* e) const {
     const QBase b = qbase(it);
-    dma16<3>(rdy, lds_addr(e + wave * 1024), a_off(b));
+    // Once for all the loads (26.2 us at n64 28x28 c512 k512 g32 3x3 stride 2;
+    // 27.0 with the wait states before each).
+    __amdgpu_buffer_rsrc_t rdy_ = rdy, rx_ = rx;
+    settle(rdy_, rx_);
+    dma16(rdy_, lds_addr(e + wave * 1024), a_off(b));
 #pragma unroll
-    for (int j = 0; j < TAPS; ++j) dma16<3>(rx, lds_addr(e + (1 + j) * PLANE + wave * 1024), b_off(b, j));
+    for (int j = 0; j < TAPS; ++j) dma16(rx_, lds_addr(e + (1 + j) * PLANE + wave * 1024), b_off(b, j));
   }
 };
 
