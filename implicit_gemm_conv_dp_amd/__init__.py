@@ -28,7 +28,8 @@ from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  
                    skg_run_wgrad, skg_tile_info, skg_gemm_workspace_bytes, skg_wgrad_workspace_bytes,
                    skg_fixup_timeouts, skg_run_wgrad_static, skg_plan_fwd, skg_plan_dgrad,
                    skg_run_fwd, skg_run_dgrad, skg_run_rmsnorm, skg_run_rmsnorm_bwd,
-                   skg_rmsnorm_bwd_workspace_bytes, skg_run_mx_quant, skg_run_mx_dequant, MODES,
+                   skg_plan_run_rmsnorm_bwd, skg_rmsnorm_bwd_workspace_bytes,
+                   skg_run_mx_quant, skg_run_mx_dequant, MODES,
                    REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS)
 
 __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd", "plan_dgrad",
@@ -42,7 +43,8 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "skg_run_wgrad_static", "skg_plan_fwd", "skg_plan_dgrad", "skg_run_fwd",
            "skg_run_dgrad", "rmsnorm", "rmsnorm_bwd", "mx_quant", "mx_dequant",
            "rmsnorm_args", "rmsnorm_bwd_args", "mx_args", "skg_run_rmsnorm",
-           "skg_run_rmsnorm_bwd", "skg_rmsnorm_bwd_workspace_bytes", "skg_run_mx_quant",
+           "skg_run_rmsnorm_bwd", "skg_plan_run_rmsnorm_bwd", "skg_rmsnorm_bwd_workspace_bytes",
+           "skg_run_mx_quant",
            "skg_run_mx_dequant"]
 
 
@@ -295,16 +297,16 @@ def rmsnorm_bwd(dy, h, rstd, dx, workspace=None, stream=None, **kw):
     """Enqueue the norm's gradient on ``stream``: dx (plus ``dres``) and the
     fp32 weight gradient ``dw``; either may be None."""
     args = rmsnorm_bwd_args(dy, h, rstd, dx, **kw)
-    ws, need = workspace, 0
-    if ws is not None:
-        need = ws.numel() * ws.element_size()
-    elif args.dw:
-        need = skg_rmsnorm_bwd_workspace_bytes(args)
-        if need:
-            import torch
-            with _pool_of(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=kw["dw"].device)
-    skg_run_rmsnorm_bwd(args, _ptr(ws), need, _handle(stream))
+    if workspace is not None:
+        skg_run_rmsnorm_bwd(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            _handle(stream))
+        return
+    need, launched = skg_plan_run_rmsnorm_bwd(args, 0, 0, _handle(stream))
+    if not launched:
+        import torch
+        with _pool_of(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=kw["dw"].device)
+        skg_run_rmsnorm_bwd(args, ws.data_ptr(), need, _handle(stream))
 
 
 def mx_quant(x, q, scales, stream=None, **kw):

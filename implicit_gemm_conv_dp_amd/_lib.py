@@ -170,6 +170,10 @@ EXPORTS = {
                                                        ctypes.POINTER(ctypes.c_size_t)]),
     "skg_run_rmsnorm_bwd": (ctypes.c_int, [ctypes.POINTER(skg_norm_bwd_args_t), ctypes.c_void_p,
                                            ctypes.c_size_t, ctypes.c_void_p]),
+    "skg_plan_run_rmsnorm_bwd": (ctypes.c_int, [ctypes.POINTER(skg_norm_bwd_args_t), ctypes.c_void_p,
+                                                ctypes.c_size_t, ctypes.c_void_p,
+                                                ctypes.POINTER(ctypes.c_size_t),
+                                                ctypes.POINTER(ctypes.c_int32)]),
     "skg_run_mx_quant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
     "skg_run_mx_dequant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
 }
@@ -324,6 +328,14 @@ def skg_rmsnorm_bwd_workspace_bytes(args):
 
 def skg_run_rmsnorm_bwd(args, ws_ptr, ws_bytes, stream_ptr):
     return check(load().skg_run_rmsnorm_bwd(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))
+
+
+def skg_plan_run_rmsnorm_bwd(args, ws_ptr, ws_bytes, stream_ptr):
+    """(bytes of workspace that the call takes, whether it was launched)."""
+    need, launched = ctypes.c_size_t(), ctypes.c_int32()
+    check(load().skg_plan_run_rmsnorm_bwd(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr,
+                                          ctypes.byref(need), ctypes.byref(launched)))
+    return need.value, launched.value
 
 
 def skg_run_mx_quant(args, stream_ptr):

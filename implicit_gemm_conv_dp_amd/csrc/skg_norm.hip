@@ -401,7 +401,16 @@ __global__ __launch_bounds__(S::THREADS) void rmsnorm_bwd_kernel(NormBwdParams p
 // Few rows, both gradients at once: the first workgroups take the rows (dx), the
 // others 32 columns each (dw), which read dy and h again, from the cache.
 // One launch and no workspace instead of two and one.
-constexpr int kSmallThreads = 1024, kRuns = 32, kSmallCols = 16384;
+constexpr int kSmallThreads = 1024, kRuns = 32, kSmallCols = 16384, kSmallRows = 1024, kSmallElements = 1 << 20;
+
+template <int N>
+SKG_DEV float tree_sum(float (&v)[N]) {
+#pragma unroll
+  for (int n = N / 2; n; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] += v[k + n];
+  return v[0];
+}
 
 template <int DT, class S, int TAIL>
 SKG_DEV void norm_bwd_row(const NormBwdParams& p, SKG_LDS uint32_t* slots) {
@@ -451,30 +460,42 @@ SKG_DEV void norm_bwd_row(const NormBwdParams& p, SKG_LDS uint32_t* slots) {
   }
 }
 
-// Thread (run, column) adds rows run, run + 32, ..., eight at a time in flight;
-// then the runs, in order.
-template <int DT>
+// dw of a few rows with the bits that norm_dw_kernel gives: thread (run, column)
+// makes the partial sums run, run + 32, ..., of the rows that one workgroup of
+// rmsnorm_bwd_kernel takes (it has a single round of them at these sizes), eight
+// rows at a time in flight, and adds both as the two kernels do.
+template <int DT, int GROUPS>
 SKG_DEV void norm_dw_columns(const NormBwdParams& p, int block, SKG_LDS float* part) {
   typedef typename Elem<DT>::raw raw;
+  constexpr int MOST = kSmallRows / kRuns;
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c0 = block * 32 + lane, c = min(c0, p.cols - 1);
   const raw* dy = reinterpret_cast<const raw*>(p.dy) + c;
   const raw* h = reinterpret_cast<const raw*>(p.h) + c;
-  float sum = 0.f;
-  for (int row = run; row < p.rows; row += 8 * kRuns) {
-    raw a[8], b[8];
-    float s[8];
+  auto row_of = [&](int i) { return (run + i / GROUPS * kRuns) * GROUPS + i % GROUPS; };
+  float v[MOST];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t r = min(row + k * kRuns, p.rows - 1);
-      a[k] = dy[r * p.lddy];
-      b[k] = h[r * p.ldh];
-      s[k] = p.rstd[r];
+  for (int k = 0; k < MOST; ++k) v[k] = 0.f;
+#pragma unroll
+  for (int i0 = 0; i0 < MOST; i0 += 8) {
+    if (row_of(i0) < p.rows) {
+      raw a[8], b[8];
+      float s[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t r = min(row_of(i0 + i), p.rows - 1);
+        a[i] = dy[r * p.lddy];
+        b[i] = h[r * p.ldh];
+        s[i] = p.rstd[r];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = (i0 + i) / GROUPS;
+        const float t = __builtin_fmaf(Elem<DT>::get(a[i]), Elem<DT>::get(b[i]) * s[i], 0.f);
+        v[k] = row_of(i0 + i) < p.rows ? v[k] + t : v[k];
+      }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      sum = row + k * kRuns < p.rows ? __builtin_fmaf(Elem<DT>::get(a[k]), Elem<DT>::get(b[k]) * s[k], sum) : sum;
   }
-  part[run * 33 + lane] = sum;
+  part[run * 33 + lane] = tree_sum(v);
   __syncthreads();
   if (run == 0 && c0 < p.cols) {
     float total = 0.f;
@@ -487,7 +508,7 @@ SKG_DEV void norm_dw_columns(const NormBwdParams& p, int block, SKG_LDS float* p
 template <int DT, class S>
 __global__ __launch_bounds__(kSmallThreads) void rmsnorm_bwd_small_kernel(NormBwdParams p, int row_blocks) {
   __shared__ float lds[kRuns * 33];
-  if ((int)blockIdx.x >= row_blocks) return norm_dw_columns<DT>(p, blockIdx.x - row_blocks, (SKG_LDS float*)lds);
+  if ((int)blockIdx.x >= row_blocks) return norm_dw_columns<DT, S::GROUPS>(p, blockIdx.x - row_blocks, (SKG_LDS float*)lds);
   SKG_LDS uint32_t* slots = (SKG_LDS uint32_t*)(SKG_LDS float*)lds;
   if (!(p.cols & 7)) return norm_bwd_row<DT, S, 0>(p, slots);
   if constexpr (S::COLS == kSmallSpread) {
@@ -502,7 +523,7 @@ __global__ __launch_bounds__(kSmallThreads) void rmsnorm_bwd_small_kernel(NormBw
 // (512 x 4096: 4 us; one column a thread over all groups took 32).
 // Without groups (no rows) it writes zeros.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ partial, float* __restrict__ dw, int groups, int cols) {
-  constexpr int RUNS = 32, MOST = kMostGroups / RUNS;
+  constexpr int RUNS = kRuns, MOST = kMostGroups / RUNS;
   __shared__ float part[RUNS][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = min((int)blockIdx.x * 32 + lane, cols - 1);
@@ -512,11 +533,7 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
     const int g = run + k * RUNS;
     v[k] = g < groups ? partial[(int64_t)g * cols + c] : 0.f;
   }
-#pragma unroll
-  for (int n = MOST / 2; n; n >>= 1)
-#pragma unroll
-    for (int k = 0; k < n; ++k) v[k] += v[k + n];
-  part[run][lane] = v[0];
+  part[run][lane] = tree_sum(v);
   __syncthreads();
   if (run == 0 && (int)blockIdx.x * 32 + lane < cols) {
     float sum = 0.f;
@@ -658,10 +675,9 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // columns' share reads dy and h a second time, which is cheaper than a second
 // launch and the partial sums (509x1111 f32 5.9 us a call against 9.2,
 // 1000x1024 bf16 7.1 against 9.7; even at 1024x4096).  Not where dx is written
-// over what that share reads; and larger calls give dw the same bits whether
-// or not it is.
+// over what that share reads; dw has the same bits in both.
 bool bwd_small(const skg_norm_bwd_args_t* a) {
-  if (!a->dw || a->rows < 1 || a->rows > 1024 || a->cols > kSmallCols || a->rows * a->cols > 1 << 20) return false;
+  if (!a->dw || a->rows < 1 || a->rows > kSmallRows || a->cols > kSmallCols || a->rows * a->cols > kSmallElements) return false;
   if (!a->dx) return true;
   const size_t es = elem_bytes(a->dtype);
   auto bytes = [&](int64_t ld) { return ((a->rows - 1) * ld + a->cols) * es; };
@@ -673,13 +689,20 @@ int bwd_groups(const skg_norm_bwd_args_t* a) {
   with_spread(a->cols, [&](auto s) {
     typedef decltype(s) S;
     static_assert(S::MOST <= kMostGroups, "what norm_dw_kernel adds");
+    static_assert(S::GROUPS * S::MOST >= kSmallRows || (S::COLS / 2 + 1) * (int64_t)S::GROUPS * S::MOST >= kSmallElements,
+                  "norm_dw_columns: a single round of rows at its sizes");
     groups = ceil_div(a->rows, S::GROUPS);
     if (groups > S::MOST) groups = S::MOST;
   });
   return (int)groups;
 }
 
-int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStream_t st) {
+size_t bwd_bytes(const skg_norm_bwd_args_t* a) { return a->dw ? size_t(bwd_groups(a)) * a->cols * 4 : 0; }
+
+// out, launched: what the call takes is wanted, and a workspace too small for
+// it is not an error but leaves the call undone.
+int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStream_t st, size_t* out = nullptr,
+                 int32_t* launched = nullptr) {
   int rc = check_norm_bwd(a);
   if (rc) return rc;
   if (a->rows > 0 && (!a->dy || !a->h || !a->rstd)) return unsupported("null dy, h or rstd");
@@ -690,7 +713,12 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
     return unsupported("pointers must be aligned to their elements");
   const int groups = bwd_groups(a);
   const bool small = bwd_small(a);
-  const size_t need = a->dw && !small ? size_t(groups) * a->cols * 4 : 0;
+  const size_t need = small ? 0 : bwd_bytes(a);
+  if (out) *out = need;
+  if (launched) {
+    *launched = need <= ws_bytes;
+    if (!*launched) return SKG_OK;
+  }
   if (need > ws_bytes) return unsupported("workspace too small for this call");
   if (need && (!ws || !aligned_to(ws, 16))) return unsupported("workspace must be 16-byte aligned device memory");
   int cus = 0;
@@ -714,7 +742,7 @@ int run_norm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, hipStr
     p.ldr = a->lddres;
     p.lddx = a->lddx;
     p.inv_cols = 1.f / (float)a->cols;
-      if (a->dtype == SKG_F16)
+    if (a->dtype == SKG_F16)
       launch_norm_bwd<DT_F16>(p, groups, small, st);
     else if (a->dtype == SKG_BF16)
       launch_norm_bwd<DT_BF16>(p, groups, small, st);
@@ -756,7 +784,7 @@ int skg_rmsnorm_bwd_workspace_bytes(const skg_norm_bwd_args_t* a, size_t* out) {
     const int rc = check_norm_bwd(a);
     if (rc) return rc;
     if (!out) return unsupported("null output");
-    *out = a->dw && !bwd_small(a) ? size_t(bwd_groups(a)) * a->cols * 4 : 0;
+    *out = bwd_bytes(a);
     return SKG_OK;
   } catch (...) {
     return hip_failure("exception in skg_rmsnorm_bwd_workspace_bytes");
@@ -767,6 +795,20 @@ int skg_run_rmsnorm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes,
   try {
     clear_error();
     return run_norm_bwd(a, ws, ws_bytes, static_cast<hipStream_t>(stream));
+  } catch (const std::exception& ex) {
+    return hip_failure(std::string("exception: ") + ex.what());
+  } catch (...) {
+    return hip_failure("unknown exception");
+  }
+}
+
+int skg_plan_run_rmsnorm_bwd(const skg_norm_bwd_args_t* a, void* ws, size_t ws_bytes, void* stream, size_t* need,
+                             int32_t* launched) {
+  try {
+    clear_error();
+    if (!need || !launched) return unsupported("null output");
+    *launched = 0;
+    return run_norm_bwd(a, ws, ws_bytes, static_cast<hipStream_t>(stream), need, launched);
   } catch (const std::exception& ex) {
     return hip_failure(std::string("exception: ") + ex.what());
   } catch (...) {

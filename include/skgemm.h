@@ -531,9 +531,10 @@ typedef struct skg_norm_args {
  *   dx = s * (g - h s^2 mean(g h)) + dres   (the gradient of x and of the
  *        residual alike; dres, or NULL, is what reaches h from above);
  *   dw = sum over rows of dy * h * s        fp32, in a fixed order.
- * A quantised y passes its gradient through unchanged.  dx (which may be dy
- * or dres) or dw may be NULL.  The workspace holds partial sums of dw; few
- * rows take none. */
+ * A quantised y passes its gradient through unchanged.  dx (which may be dy,
+ * h or dres) or dw may be NULL.  The workspace holds partial sums of dw; a few
+ * rows take none unless dx is written over dy or h.  dw has the same bits
+ * either way. */
 typedef struct skg_norm_bwd_args {
   int64_t rows, cols;
   int32_t dtype;           /* dy, h, dres, dx */
@@ -576,8 +577,14 @@ typedef struct skg_mx_args {
 } skg_mx_args_t;
 
 int skg_run_rmsnorm(const skg_norm_args_t* args, void* stream);
+/* A workspace that is enough wherever dx goes: by rows, cols and whether dw is
+ * wanted, the other pointers are not looked at. */
 int skg_rmsnorm_bwd_workspace_bytes(const skg_norm_bwd_args_t* args, size_t* out);
 int skg_run_rmsnorm_bwd(const skg_norm_bwd_args_t* args, void* ws, size_t ws_bytes, void* stream);
+/* Fills *need with what this very call takes and runs it if ws_bytes is enough
+ * for it (*launched 1).  Otherwise nothing is enqueued (*launched 0, status 0). */
+int skg_plan_run_rmsnorm_bwd(const skg_norm_bwd_args_t* args, void* ws, size_t ws_bytes, void* stream,
+                             size_t* need, int32_t* launched);
 int skg_run_mx_quant(const skg_mx_args_t* args, void* stream);
 int skg_run_mx_dequant(const skg_mx_args_t* args, void* stream);
 
