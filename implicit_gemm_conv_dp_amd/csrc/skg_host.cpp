@@ -9,6 +9,7 @@
 // commits sizing the default pool, and the bot comment on automatic selection
 // (a remainder with fewer iterations than the pool gives no stream-K CTAs).
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include <algorithm>
@@ -151,6 +152,9 @@ int resolve_sk_order(int requested, bool wgrad) {
   return wgrad ? SKG_SK_ORDER_KMAJOR : SKG_SK_ORDER_BLOCK;
 }
 
+// The fp4 tiles of the ring kernel; the others are the direct kernel's.
+static bool ring_tile(const TileDesc& t) { return (t.gemm_mask & M_F4) && t.tk == 256; }
+
 int plan_launch(const GemmShape& g, const TileDesc& t, int mode, int reduction, int ctas,
                 int sk_order, int num_cus, int resident_per_cu, skg_plan_t* out) {
   const int requested = mode;
@@ -164,6 +168,9 @@ int plan_launch(const GemmShape& g, const TileDesc& t, int mode, int reduction, 
   if (rc) return rc;
   rc = make_plan(g, t, mode, reduction, ctas, num_cus, resident_per_cu, out);
   if (rc) return rc;
+  // (fp4 ring tiles: a workgroup a CU walks the plan's grid.)
+  if (!(ring_tile(t) && out->mode == SKG_MODE_DP) && out->grid * t.n_waves * 64 > int64_t(kMostThreads))
+    return unsupported("too many workgroups for one launch");
   out->requested_mode = requested;
   out->slices = slices;
   // Slice-major order needs every stream-K CTA to hold one whole slice of
@@ -356,9 +363,11 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   for (int id = 0; id < SKG_TILE_COUNT; ++id) {
     const TileDesc& t = kTiles[id];
     if (!(t.gemm_mask & M_F4) || (t.dp_only && !dp)) continue;
-    const double rounds = (double)ceil_div(ceil_div(r.M, t.tm) * ceil_div(r.N, t.tn), 256);  // CUs of a gfx950
+    const double tiles = (double)ceil_div(r.M, t.tm) * (double)ceil_div(r.N, t.tn);
+    if (!ring_tile(t) && tiles * t.n_waves * 64 > kMostThreads) continue;
+    const double rounds = std::ceil(tiles / 256);  // CUs of a gfx950
     double us;
-    if (t.tk == 512) {
+    if (!ring_tile(t)) {
       const int64_t rows = std::min<int64_t>(t.tm, r.M) + std::min<int64_t>(t.tn, r.N);
       const double bytes = (double)rows * (double)r.K * (0.5 + 1.0 / 32);
       const double start = std::max(0, t.tm + t.tn - 60) * 0.036, least = (t.tm + t.tn - 18) * 0.04;

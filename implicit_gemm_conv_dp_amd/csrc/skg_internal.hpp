@@ -18,6 +18,9 @@ int unsupported(const std::string& msg);
 // Returns -1 after recording msg.
 int hip_failure(const std::string& msg);
 
+// Most threads of one launch: the runtime takes fewer than 2^32 along an axis.
+constexpr uint32_t kMostThreads = UINT32_MAX;
+
 // CU count of the current device; -1 without one, -2 if it is not gfx950.
 int check_device(int* cus);
 

@@ -23,6 +23,7 @@ struct MxParams {
   uint8_t* sc;
   int64_t rows, cols, kq;  // kq: elements written along the quantised axis
   int64_t ldx, ldq;        // elements
+  uint32_t first;          // along the columns: tile of the launch's first workgroup
 };
 
 // Along the rows and reading back: U chunks of eight elements a thread, four
@@ -151,11 +152,11 @@ SKG_DEV void mx_quant_t_tile(const MxParams& p, SKG_LDS char* tile) {
     raw v[4];
   };
   auto at = [&](int r, int g) { return tile + r * P + (ES == 2 ? g ^ ((r >> 5 & 1) << 2) : g) * GB; };
-    // Tiles of the same rows follow one another, so that x's rows are read
+  // Tiles of the same rows follow one another, so that x's rows are read
   // through (the other order took 50 us for 42 at 8192x8192 bf16 to e2m1, on
   // tiles of 64 columns).
-  const uint32_t across = (uint32_t)((p.cols + TC - 1) / TC), down = blockIdx.x / across;
-  const int64_t r0 = (int64_t)down * TR, c0 = (int64_t)(blockIdx.x - down * across) * TC;
+  const uint32_t id = p.first + blockIdx.x, across = (uint32_t)((p.cols + TC - 1) / TC), down = id / across;
+  const int64_t r0 = (int64_t)down * TR, c0 = (int64_t)(id - down * across) * TC;
   constexpr int N = TR * TC / 8 / T::THREADS;
   Chunk<DT> in[N];
 #pragma unroll
@@ -250,6 +251,7 @@ int run_mx(const skg_mx_args_t* a, bool quant, hipStream_t st) {
   p.kq = a->kq;
   p.ldx = a->ldx;
   p.ldq = a->ldq;
+  p.first = 0;
   auto by_type = [&](auto launch) {
     auto by_fmt = [&](auto dt) {
       if (f4)
@@ -267,9 +269,16 @@ int run_mx(const skg_mx_args_t* a, bool quant, hipStream_t st) {
   if (a->transpose) {
     const int64_t tiles = ceil_div(a->kq, kTRows) * ceil_div(a->cols, kTCols);
     if (tiles > INT32_MAX) return unsupported("too many tiles to transpose");
-    const dim3 grid((unsigned)tiles);
+    // Tiles in launches of fewer than 2^32 threads.
     by_type([&](auto dt, auto f4_) {
-      hipLaunchKernelGGL((mx_quant_t_kernel<decltype(dt)::value, decltype(f4_)::value>), grid, dim3(TTile<decltype(dt)::value>::THREADS), 0, st, p);
+      constexpr int DT = decltype(dt)::value, THREADS = TTile<DT>::THREADS;
+      constexpr int64_t most = kMostThreads / THREADS;
+      for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+        MxParams q = p;
+        q.first = (uint32_t)t0;
+        hipLaunchKernelGGL((mx_quant_t_kernel<DT, decltype(f4_)::value>), dim3((unsigned)std::min(most, tiles - t0)),
+                           dim3(THREADS), 0, st, q);
+      }
     });
   } else {
     Walk w;
@@ -287,7 +296,7 @@ int run_mx(const skg_mx_args_t* a, bool quant, hipStream_t st) {
       q.sc += r0 * (a->kq / 32);
       // Many chunks: four a thread (8192x8192 bf16 to e2m1 33 us, 5.2 TB/s,
       // and back 32).  Few: one, for the sake of more workgroups.
-            const int u = w.chunks >= (1u << 20) ? 4 : 1;
+      const int u = w.chunks >= (1u << 20) ? 4 : 1;
       const dim3 grid((unsigned)ceil_div(w.chunks, 256 * u));
       by_type([&](auto dt, auto f4_) {
         constexpr int DT = decltype(dt)::value;

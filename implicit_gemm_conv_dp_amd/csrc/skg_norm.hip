@@ -15,6 +15,7 @@
 // reaches 5.2 to 5.4 TB/s here, two reads and a write 5.8 to 5.9.  Measured:
 // 8192x8192 bf16 with a residual to e4m3 with row scales 81 us (5.8 TB/s), 4864x4096 to bf16
 // 31 us (5.1), gradient of 16384x4096 bf16 with a residual 102 us (5.3).
+#include <algorithm>
 #include <exception>
 #include <string>
 
@@ -558,13 +559,25 @@ void with_spread(int64_t cols, F&& f) {
 }
 
 template <int DT, class S>
-void launch_norm(const NormParams& p, int out, hipStream_t st) {
-  const dim3 grid((unsigned)ceil_div(p.rows, S::GROUPS)), block(S::THREADS);
-  switch (out) {
-    case OUT_SAME: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_SAME, S>), grid, block, 0, st, p); break;
-    case OUT_E4M3_ROW: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_ROW, S>), grid, block, 0, st, p); break;
-    case OUT_E4M3_MX: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_MX, S>), grid, block, 0, st, p); break;
-    default: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E2M1_MX, S>), grid, block, 0, st, p);
+void launch_norm(const NormParams& all, int out, hipStream_t st) {
+  // Rows in launches of fewer than 2^32 threads.
+  constexpr int64_t most = int64_t(kMostThreads / S::THREADS) * S::GROUPS, es = sizeof(typename Elem<DT>::raw);
+  for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
+    NormParams p = all;
+    p.rows = (int)std::min<int64_t>(most, all.rows - r0);
+    p.x += r0 * p.ldx * es;
+    if (p.r) p.r += r0 * p.ldr * es;
+    if (p.h) p.h += r0 * p.ldh * es;
+    if (p.rstd) p.rstd += r0;
+    p.y += out == OUT_SAME ? r0 * p.ldy * es : out == OUT_E2M1_MX ? r0 * (p.ldy / 2) : r0 * p.ldy;
+    if (out != OUT_SAME) p.scale = static_cast<char*>(p.scale) + r0 * (out == OUT_E4M3_ROW ? 4 : p.cols / 32);
+    const dim3 grid((unsigned)ceil_div(p.rows, S::GROUPS)), block(S::THREADS);
+    switch (out) {
+      case OUT_SAME: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_SAME, S>), grid, block, 0, st, p); break;
+      case OUT_E4M3_ROW: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_ROW, S>), grid, block, 0, st, p); break;
+      case OUT_E4M3_MX: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E4M3_MX, S>), grid, block, 0, st, p); break;
+      default: hipLaunchKernelGGL((rmsnorm_kernel<DT, OUT_E2M1_MX, S>), grid, block, 0, st, p);
+    }
   }
 }
 template <int DT>
