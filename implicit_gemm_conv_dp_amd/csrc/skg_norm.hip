@@ -107,12 +107,17 @@ SKG_DEV void place_row(Chunk<DT> (&c)[S::NCH], int t, int cols) {
 }
 
 // 1 / sqrt(v) within half an ulp or so: the hardware's reciprocal square
-// root and one Newton step.  0 for an infinite v, NaN for a NaN.
+// root and one Newton step.  A subnormal v, which the instruction takes for
+// zero, is scaled by an even power of two.  Infinite for a zero, 0 for an
+// infinite v, NaN for a NaN.
 SKG_DEV float rsqrt_refined(float v) {
-  const float r = __builtin_amdgcn_rsqf(v);
-  const float e = __builtin_fmaf(-v * r, r, 1.f);
+  const bool small = v < 0x1p-126f;
+  const float u = small ? v * 0x1p+64f : v;
+  const float r = __builtin_amdgcn_rsqf(u);
+  const float e = __builtin_fmaf(-u * r, r, 1.f);
   const float n = __builtin_fmaf(0.5f * r, e, r);
-  return r > 0.f && v < 3e38f ? n : r;
+  const float f = u > 0.f && u < 3e38f ? n : r;
+  return small ? f * 0x1p+32f : f;
 }
 
 // What is done with a row once it is summed and stored: y in its type.

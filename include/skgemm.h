@@ -499,6 +499,7 @@ int skg_fixup_timeouts(uint32_t* count, int32_t reset);
  *   h = round(x + residual)       in the rows' type (h = x without residual);
  *   s = 1 / sqrt(mean(h^2) + eps) fp32 (stored in rstd for the gradient);
  *   y = h * s * weight            (weight 1 when NULL).
+ * eps may be zero; an empty row then has s infinite and y NaN.
  * y is written
  *   - in the rows' type (dtype_y == dtype), rounded once;
  *   - as e4m3 codes of y / d with one fp32 scale d = max(max|y| / 448, 2^-126)
