@@ -215,6 +215,19 @@ hipError_t zero_fill(void* p, size_t bytes, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The same for `rows` rows of `words` words at a pitch of `pitch` words.
+__global__ __launch_bounds__(256) void zero_rows_kernel(uint32_t* p, size_t rows, size_t words, size_t pitch) {
+  for (size_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (size_t i = threadIdx.x; i < words; i += blockDim.x) p[r * pitch + i] = 0u;
+}
+
+hipError_t zero_rows(void* p, size_t rows, size_t words, size_t pitch, hipStream_t st) {
+  if (words == pitch) return zero_fill(p, rows * words * 4, st);
+  hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)(rows < 16384 ? rows : 16384)), dim3(256), 0, st,
+                     static_cast<uint32_t*>(p), rows, words, pitch);
+  return hipGetLastError();
+}
+
 // Scratch of skg_run_wgrad_static: a file-scope device array (one copy per
 // device the library runs on, held until the process ends).  Host code
 // never uses the array's name as a device address: the address of each
@@ -506,8 +519,9 @@ int run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* strea
   rc = check_run(pl, ws, ws_bytes, cus, per_cu);
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a->dtype_ab == SKG_F4E2M1 && pl.reduction != SKG_RED_ATOMIC) {
-    // Kernel resets, so that the call may be captured into a graph.
+  // fp4: kernel resets, so that the call may be captured into a graph.
+  const bool kernel_resets = a->dtype_ab == SKG_F4E2M1;
+  if (kernel_resets) {
     const size_t bytes = !pl.sk_ctas ? 0 : (size_t)(handoff_reduction(pl.reduction) ? pl.flags_bytes : pl.workspace_bytes);
     hipError_t e = zero_fill(ws, bytes, st);
     if (e != hipSuccess) return hip_failure(std::string("reset: ") + hipGetErrorString(e));
@@ -516,7 +530,8 @@ int run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* strea
     if (rc) return rc;
   }
   if (pl.reduction == SKG_RED_ATOMIC && pl.sk_ctas) {
-    hipError_t e = hipMemset2DAsync(a->C, (size_t)a->ldc * 4, 0, (size_t)a->N * 4, (size_t)a->M, st);
+    hipError_t e = kernel_resets ? zero_rows(a->C, (size_t)a->M, (size_t)a->N, (size_t)a->ldc, st)
+                                 : hipMemset2DAsync(a->C, (size_t)a->ldc * 4, 0, (size_t)a->N * 4, (size_t)a->M, st);
     if (e != hipSuccess) return hip_failure(std::string("zeroing C: ") + hipGetErrorString(e));
   }
   GemmParams g;
