@@ -164,6 +164,8 @@ def _handle(stream):
         return stream.cuda_stream
     if _current_handle is None:
         import torch
+        if not torch.cuda.is_initialized():
+            return 0  # nothing has made another stream the current one
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         device = getattr(torch._C, "_cuda_getDevice", None)
         if raw and device:
