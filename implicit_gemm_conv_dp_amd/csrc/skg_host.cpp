@@ -418,6 +418,8 @@ int validate_gemm(const skg_gemm_args_t* a) {
     return unsupported("atomic reduction needs an fp32 output");
   if (a->M <= 0 || a->N <= 0 || a->K <= 0) return unsupported("M, N and K must be positive");
   if (a->M > INT32_MAX || a->N > INT32_MAX || a->K > INT32_MAX) return unsupported("dimension too large");
+  // (The fp4 kernels compare the ends of tiles of up to 256 in 32 bits.)
+  if (a->dtype_ab == SKG_F4E2M1 && (a->M > INT32_MAX - 255 || a->N > INT32_MAX - 255)) return unsupported("dimension too large");
   if (a->lda < a->K || a->ldb < a->K || a->ldc < a->N) return unsupported("leading dimension too small");
   const int bits = elem_bits(a->dtype_ab), ec = elem_bytes(a->dtype_c);
   if (a->dtype_ab == SKG_F4E2M1 && a->ldc > INT32_MAX) return unsupported("leading dimension too large");
