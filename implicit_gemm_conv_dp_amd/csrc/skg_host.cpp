@@ -338,6 +338,11 @@ int64_t dgrad_filter_bytes(const skg_conv_args_t* a) {
   return ceil_div(int64_t(a->k) * a->r * a->s * (a->c / a->groups) * 2, 256) * 256;
 }
 
+// Whether 32-bit offsets reach a tile's last rows.
+static bool spans_rows(const TileDesc& t, const skg_gemm_args_t* a) {
+  return row_bytes(a->dtype_ab, a->lda) <= kMaxBufferBytes / t.tm && row_bytes(a->dtype_ab, a->ldb) <= kMaxBufferBytes / t.tn;
+}
+
 // The fp4 tile of a call that leaves it open: the least of the times that these
 // models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
 // 8192, K 256 to 8192) on all tiles.  On 73 others drawn over these ranges the
@@ -362,7 +367,7 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   double best = 1e300;
   for (int id = 0; id < SKG_TILE_COUNT; ++id) {
     const TileDesc& t = kTiles[id];
-    if (!(t.gemm_mask & M_F4) || (t.dp_only && !dp)) continue;
+    if (!(t.gemm_mask & M_F4) || (t.dp_only && !dp) || !spans_rows(t, &r)) continue;
     const double tiles = (double)ceil_div(r.M, t.tm) * (double)ceil_div(r.N, t.tn);
     if (!ring_tile(t) && tiles * t.n_waves * 64 > kMostThreads) continue;
     const double rounds = std::ceil(tiles / 256);  // CUs of a gfx950
@@ -426,7 +431,7 @@ int validate_gemm(const skg_gemm_args_t* a) {
   if ((a->K * bits) % 128 || (a->lda * bits) % 128 || (a->ldb * bits) % 128)
     return unsupported("K, lda and ldb must be multiples of 16 bytes");
   if ((a->ldc * ec) % 16) return unsupported("ldc must be a multiple of 16 bytes");
-  if (t->tm * row_bytes(a->dtype_ab, a->lda) > kMaxBufferBytes || t->tn * row_bytes(a->dtype_ab, a->ldb) > kMaxBufferBytes)
+  if (!spans_rows(*t, a))
     return unsupported("row pitch too large for 32-bit tile offsets");
   return SKG_OK;
 }
