@@ -291,7 +291,8 @@ def mx_args(x=None, q=None, scales=None, *, rows, cols, dtype, dtype_q, kq=None,
 def rmsnorm(x, y, stream=None, **kw):
     """Enqueue y = norm(x + residual) * weight on ``stream``; ``h`` receives
     the sum, ``rstd`` the rows' factors for ``rmsnorm_bwd``, ``y_scale`` the
-    scales of a quantised output (``dtype_y``)."""
+    scales of a quantised output (``dtype_y``).  MX blocks (``scale_mode="mx"``)
+    take ``cols`` a multiple of 32; an MX product of them a multiple of 128."""
     skg_run_rmsnorm(rmsnorm_args(x, y, **kw), _handle(stream))
 
 

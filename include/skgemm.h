@@ -507,7 +507,9 @@ int skg_fixup_timeouts(uint32_t* count, int32_t reset);
  *     of skg_run_gemm).  A NaN or infinity in a row gives it a scale of NaN;
  *   - as MX blocks (SKG_F8E4M3 or SKG_F4E2M1 with SKG_SCALE_MX_E8M0; cols a
  *     multiple of 32, y_scale rows x cols/32 E8M0 codes), as skg_run_mx_quant
- *     makes them from the fp32 y. */
+ *     makes them from the fp32 y.  They are A and scale_a of skg_run_gemm where
+ *     cols is a multiple of 128, as its MX products need; for other widths
+ *     write y in the rows' type and let skg_run_mx_quant pad (kq). */
 typedef struct skg_norm_args {
   int64_t rows, cols;
   int32_t dtype;           /* x, residual, h: SKG_F16, SKG_BF16 or SKG_F32 */
