@@ -10,10 +10,11 @@
 //
 // Used where the 128-row and 256-row tiles would leave most of the device
 // idle: the time there is the latency of one tile's reduction, which this
-// form cuts by four waves.  It is bound by how fast a CU takes its operands
-// in: 128-byte rows go straight to LDS (whole lines; loaded into the MFMA's
-// register layout, 16 rows of 64 bytes an instruction, the same rows came in at half
-// that rate).
+// form cuts by four waves.  128-byte rows go straight to LDS (whole lines;
+// loaded into the MFMA's register layout, 16 rows of 64 bytes an instruction,
+// the same rows came in at half the rate).  With two stages a wave in flight a
+// CU takes in 60 kB/us; the same loads with nothing else to do reach 135, so a
+// deeper ring, for which the smaller tiles have the LDS, is what is left here.
 #pragma once
 
 #include "skg_device.hpp"
@@ -77,8 +78,9 @@ struct F4Direct {
                  : "memory", "m0", "scc");
   }
   // Scale DMA n of chunk c (A's, then B's): eight rows of eight words of four
-  // scales.  Words past K are zeros, and scale codes past K, which may be
-  // another row's, by 2^-254 in all: such products vanish in fp32.
+  // scales (K is a multiple of 128: whole words).  Words past K are zeros, so the
+  // codes that were read past K, padding or another row's, are scaled by 2^-254
+  // in all and vanish in fp32.
   template <int N>
   SKG_DEV void dma_scales(int c) const {
     if constexpr (N < CA + CB) {

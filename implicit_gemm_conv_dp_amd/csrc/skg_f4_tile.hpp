@@ -13,10 +13,12 @@
 // and DMA has its place after an MFMA of the k-step before (left to itself the
 // compiler moves the reads next to their uses, and the MFMAs wait for them).
 //
-// What bounds it: power.  64 such MFMAs of a wave take 0.87 us on an otherwise
-// idle device (2.4 GHz), 1.25 on all CUs with constant operands and 1.59 with
-// random ones, in registers and LDS alone; 5.4 PFLOP/s.  This loop takes 1.74.
-// 8192x8192x8192 to bf16 265 us (4.15 PFLOP/s): 4 x (32 iterations of 1.74 us,
+// What bounds it: power.  An iteration's 64 MFMAs of a wave, with its reads and
+// loads and operands that stay in the L2, take 0.90 us on an otherwise idle device
+// (2.42 GHz, the matrix units 93 % busy).  On all CUs the clock falls: 1.25 to
+// 1.36 us with constant operands and 1.59 to 1.73 with random ones (1.35 GHz, 88 %
+// busy), by the device: 5.0 to 5.4 PFLOP/s.  This loop takes 1.74 where that
+// takes 1.59.  8192x8192x8192 to bf16 265 to 275 us (4.15 PFLOP/s): 4 x (32 iterations,
 // 4 us of copy-out, which writes 8 TB/s, 2 us of start).  Measured without
 // gain: reading the next stages into the L2 ahead, strips of 2 or 8 tile rows,
 // refills every second or third MFMA, streaming stores.

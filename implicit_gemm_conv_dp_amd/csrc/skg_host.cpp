@@ -345,8 +345,11 @@ static bool spans_rows(const TileDesc& t, const skg_gemm_args_t* a) {
 
 // The fp4 tile of a call that leaves it open: the least of the times that these
 // models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
-// 8192, K 256 to 8192) on all tiles.  On 73 others drawn over these ranges the
-// tile it picks takes 1.5 % longer than the best one, on average.
+// 8192, K 256 to 8192) on all tiles, one call repeated: operands up to 256 MB
+// come from the last-level cache, and nothing here counts HBM (1x8192x8192, 36 MB:
+// the model says 4.0 us, a call from HBM takes 9.1).  On 73 other shapes drawn over
+// these ranges, measured in the same way, the tile it picks takes 1.5 % longer
+// than the best one, on average.
 // - A direct tile's workgroups take their operands' rows in at 60 kB/us a CU,
 //   the larger ones after a start that nothing covers (one workgroup a CU),
 //   and short reductions cost a round of workgroups its latency:

@@ -142,11 +142,12 @@ SKG_DEV void norm_output(const NormParams& p, int row, bool live, int t, float s
       if (left(i) > 0) store_chunk<DT>(y + (t + i * G) * 8, left(i), c);
     }
   } else if constexpr (OUT == OUT_E4M3_ROW) {
-    // y / d = h w 448 / max|h w|: the row's factor s cancels, and for
-    // 16-bit inputs h w and h w 448 are exact in fp32.  The quotient is
-    // rounded correctly (a reciprocal, then one residual step), so values
-    // that lie on a border between two codes, which 16-bit inputs often
-    // do, round to even and not by the noise of a scaled product.
+    // y / d = h w 448 / max|h w|: the row's factor s cancels.  For bf16 rows
+    // and weights h w 448 is exact in fp32 (with f16 or f32 the products
+    // are rounded).  The quotient is rounded to fp32 correctly (a reciprocal,
+    // then one residual step) and then to a code, so values exactly between
+    // two codes, which bf16 inputs often have (1 in 62 at 8192x8192), go to the
+    // even one and not where the noise of a scaled product takes them.
     float v[NCH][8];
     uint32_t top = 0;
 #pragma unroll
@@ -692,7 +693,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // Whether both gradients come from one launch without a workspace.  The
 // columns' share reads dy and h a second time, which is cheaper than a second
 // launch and the partial sums (509x1111 f32 5.9 us a call against 9.2,
-// 1000x1024 bf16 7.1 against 9.7; even at 1024x4096).  Not where dx is written
+// 1000x1024 bf16 6.7 against 9.7).  At 1024x4096 the two took the same time;
+// the limit lies where one launch was well ahead.  Not where dx is written
 // over what that share reads; dw has the same bits in both.
 bool bwd_small(const skg_norm_bwd_args_t* a) {
   if (!a->dw || a->rows < 1 || a->rows > kSmallRows || a->cols > kSmallCols || a->rows * a->cols > kSmallElements) return false;
