@@ -18,7 +18,7 @@
 // (2.42 GHz, the matrix units 93 % busy).  On all CUs the clock falls: 1.25 to
 // 1.36 us with constant operands and 1.59 to 1.73 with random ones (1.35 GHz, 88 %
 // busy), by the device: 5.0 to 5.4 PFLOP/s.  This loop takes 1.74 where that
-// takes 1.59.  8192x8192x8192 to bf16 265 to 275 us (4.15 PFLOP/s): 4 x (32 iterations,
+// takes 1.59.  8192x8192x8192 to bf16 256 to 275 us (4.0 to 4.3 PFLOP/s): 4 x (32 iterations,
 // 4 us of copy-out, which writes 8 TB/s, 2 us of start).  Measured without
 // gain: reading the next stages into the L2 ahead, strips of 2 or 8 tile rows,
 // refills every second or third MFMA, streaming stores.
