@@ -265,8 +265,10 @@ typedef struct skg_tile_info {
  * Alignment: A, B, C 16-byte aligned; lda, ldb multiples of 16 bytes; K a
  * multiple of 16 bytes of input type; ldc a multiple of 16 bytes; lda, ldb
  * >= K and ldc >= N (else -2).  Only the first K elements of each A row and
- * B column are read, and only the M x N elements of C are written: padding
- * columns of C keep what they held. */
+ * B column count, and only the M x N elements of C are written: padding
+ * columns of C keep what they held.  (fp4: up to 64 bytes past K of a row that
+ * has another one after it may be read; nothing past the last row's K
+ * elements.  M and N at most 2^31 - 256.) */
 typedef struct skg_gemm_args {
   int64_t M, N, K;
   int32_t dtype_ab;        /* SKG_F16, SKG_BF16, SKG_F8E4M3, SKG_F8E5M2 or SKG_F4E2M1 */
