@@ -18,9 +18,16 @@ the output as 16-bit values, e4m3 codes with row scales, or MX blocks) and
 ``rmsnorm_bwd``; ``mx_quant`` / ``mx_dequant`` to and from MX blocks of e4m3 or
 e2m1 (4-bit) codes; and ``gemm(dtype_ab="e2m1", scale_mode="mx",
 tile="auto")`` for their product.
+
+Around an 8-bit attention projection: ``block_quant`` into blocks of 128 along
+the rows, the columns or both, ``gemm(dtype_ab="e4m3", scale_mode="block128" or
+"row128", tile="auto")`` for their products, ``qknorm_rope`` and
+``qknorm_rope_bwd`` for the norms of queries and keys for each head with the
+position's rotation, and ``newton_schulz`` for the update of its weight.
 """
 
 import contextlib
+import ctypes
 
 from . import _lib
 from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  # noqa: F401
@@ -29,8 +36,11 @@ from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  
                    skg_fixup_timeouts, skg_run_wgrad_static, skg_plan_fwd, skg_plan_dgrad,
                    skg_run_fwd, skg_run_dgrad, skg_run_rmsnorm, skg_run_rmsnorm_bwd,
                    skg_plan_run_rmsnorm_bwd, skg_rmsnorm_bwd_workspace_bytes,
-                   skg_run_mx_quant, skg_run_mx_dequant, MODES,
-                   REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS)
+                   skg_run_mx_quant, skg_run_mx_dequant, skg_run_block_quant,
+                   skg_run_qknorm_rope, skg_run_qknorm_rope_bwd, skg_plan_run_qknorm_rope_bwd,
+                   skg_qknorm_rope_bwd_workspace_bytes, skg_run_newton_schulz,
+                   skg_newton_schulz_workspace_bytes, MODES,
+                   REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS, BLOCKS, ROPE_STYLES)
 
 __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd", "plan_dgrad",
            "gemm_args", "wgrad_args", "conv_args",
@@ -45,7 +55,12 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "rmsnorm_args", "rmsnorm_bwd_args", "mx_args", "skg_run_rmsnorm",
            "skg_run_rmsnorm_bwd", "skg_plan_run_rmsnorm_bwd", "skg_rmsnorm_bwd_workspace_bytes",
            "skg_run_mx_quant",
-           "skg_run_mx_dequant"]
+           "skg_run_mx_dequant", "BLOCKS", "ROPE_STYLES", "block_quant", "qknorm_rope",
+           "qknorm_rope_bwd", "newton_schulz", "block_quant_args", "qknorm_rope_args",
+           "newton_schulz_args", "skg_run_block_quant", "skg_run_qknorm_rope",
+           "skg_run_qknorm_rope_bwd", "skg_plan_run_qknorm_rope_bwd",
+           "skg_qknorm_rope_bwd_workspace_bytes", "skg_run_newton_schulz",
+           "skg_newton_schulz_workspace_bytes"]
 
 
 class _Names(dict):
@@ -67,6 +82,8 @@ _MODE = _Names(MODES, "mode")
 _REDUCTION = _Names(REDUCTIONS, "reduction")
 _SCALE_MODE = _Names(SCALE_MODES, "scale mode")
 _SK_ORDER = _Names(SK_ORDERS, "stream-K order")
+_BLOCK = _Names(BLOCKS, "block shape")
+_STYLE = _Names(ROPE_STYLES, "rotation style")
 
 
 def _ptr(t):
@@ -322,3 +339,124 @@ def mx_quant(x, q, scales, stream=None, **kw):
 def mx_dequant(q, scales, x, stream=None, **kw):
     """Enqueue x = the values of MX codes ``q`` with ``scales`` on ``stream``."""
     skg_run_mx_dequant(mx_args(x, q, scales, **kw), _handle(stream))
+
+
+def block_quant_args(x=None, q=None, scales=None, qt=None, scales_t=None, *, rows, cols, dtype,
+                     dtype_q, block="1x128", kq=None, kqt=None, ldx=None, ldq=None, ldqt=None):
+    if kq is None:
+        kq = (cols + 127) // 128 * 128
+    if kqt is None:
+        kqt = (rows + 127) // 128 * 128
+    return _lib.skg_block_quant_args_t(
+        rows, cols, kq, kqt, _DTYPE[dtype], _DTYPE[dtype_q], _BLOCK[block],
+        0 if x is None else x.data_ptr(), cols if ldx is None else ldx,
+        0 if q is None else q.data_ptr(), kq if ldq is None else ldq,
+        0 if scales is None else scales.data_ptr(),
+        0 if qt is None else qt.data_ptr(), kqt if ldqt is None else ldqt,
+        0 if scales_t is None else scales_t.data_ptr())
+
+
+def block_quant(x, q=None, scales=None, qt=None, scales_t=None, stream=None, **kw):
+    """Enqueue the quantisation of ``x`` into e4m3 or e5m2 codes with an fp32
+    scale for each block of 128 on ``stream``: ``q`` and ``scales`` along the rows,
+    ``qt`` and ``scales_t`` transposed, along the columns; either pair may be
+    None.  ``block="128x128"`` takes one scale for 128 rows too."""
+    skg_run_block_quant(block_quant_args(x, q, scales, qt, scales_t, **kw), _handle(stream))
+
+
+def qknorm_rope_args(q=None, k=None, yq=None, yk=None, dyq=None, dyk=None, *, batch=1, seq, heads_q,
+                     heads_k, head_dim, rope_dim=None, dtype, weight_q=None, weight_k=None,
+                     dtype_w=None, cos=None, sin=None, table_rows=0, positions=None, pos0=0,
+                     style="half", eps=1e-6, q_strides=None, k_strides=None, yq_strides=None,
+                     yk_strides=None, dyq_strides=None, dyk_strides=None, dwq=None, dwk=None):
+    """Strides: (batch, token, head) in elements, those of a contiguous
+    (batch, seq, heads, head_dim) tensor where None."""
+    dt = _DTYPE[dtype]
+    tq, tk = heads_q * head_dim, heads_k * head_dim
+    cq, ck = (seq * tq, tq, head_dim), (seq * tk, tk, head_dim)
+    return _lib.skg_heads_args_t(
+        batch, seq, heads_q, heads_k, head_dim, head_dim if rope_dim is None else rope_dim, dt,
+        dt if dtype_w is None else _DTYPE[dtype_w], _STYLE[style],
+        32 if positions is None else 8 * positions.element_size(),
+        0 if q is None else q.data_ptr(), 0 if k is None else k.data_ptr(),
+        q_strides or cq, k_strides or ck,
+        0 if yq is None else yq.data_ptr(), 0 if yk is None else yk.data_ptr(),
+        yq_strides or cq, yk_strides or ck,
+        0 if weight_q is None else weight_q.data_ptr(),
+        0 if weight_k is None else weight_k.data_ptr(),
+        0 if cos is None else cos.data_ptr(), 0 if sin is None else sin.data_ptr(), table_rows,
+        0 if positions is None else positions.data_ptr(), pos0,
+        0 if dyq is None else dyq.data_ptr(), 0 if dyk is None else dyk.data_ptr(),
+        dyq_strides or cq, dyk_strides or ck,
+        0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), eps)
+
+
+def qknorm_rope(q, k, yq, yk, stream=None, **kw):
+    """Enqueue the norms of queries and keys for each head and the position's
+    rotation on ``stream``.  ``cos`` and ``sin`` are fp32 tables of ``table_rows``
+    positions; ``positions`` (int32 or int64) names each token's row, without it
+    token t of a batch is at ``pos0 + t``."""
+    skg_run_qknorm_rope(qknorm_rope_args(q, k, yq, yk, **kw), _handle(stream))
+
+
+def qknorm_rope_bwd(dyq, dyk, q, k, dq, dk, workspace=None, stream=None, **kw):
+    """Enqueue the gradient of ``qknorm_rope`` on ``stream``: dq and dk (their
+    strides are ``yq_strides`` and ``yk_strides``) and the fp32 weight gradients
+    ``dwq`` and ``dwk``; each may be None."""
+    args = qknorm_rope_args(q, k, dq, dk, dyq, dyk, **kw)
+    if workspace is not None:
+        skg_run_qknorm_rope_bwd(args, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _handle(stream))
+        return
+    need, launched = skg_plan_run_qknorm_rope_bwd(args, 0, 0, _handle(stream))
+    if not launched:
+        import torch
+        dw = kw.get("dwq")
+        with _pool_of(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=(kw["dwk"] if dw is None else dw).device)
+        skg_run_qknorm_rope_bwd(args, ws.data_ptr(), need, _handle(stream))
+
+
+# The quintic whose five steps bring singular values from 0.01 .. 1 to 0.7 .. 1.2.
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz_args(g=None, out=None, *, rows, cols, dtype, dtype_out=None, steps=5,
+                       coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, scale=1.0, ldg=None,
+                       ldo=None):
+    """``coefficients``: a, b, c for every step, or a row of three for each."""
+    if coefficients and hasattr(coefficients[0], "__len__"):
+        if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
+            raise ValueError("coefficients: three numbers, or a row of three for each step")
+        flat = [v for c in coefficients for v in c]
+    else:
+        if len(coefficients) != 3:
+            raise ValueError("coefficients: three numbers, or a row of three for each step")
+        flat = list(coefficients) * steps
+    values = (ctypes.c_float * max(len(flat), 1))(*flat)
+    dt = _DTYPE[dtype]
+    a = _lib.skg_newton_schulz_args_t(
+        rows, cols, dt, dt if dtype_out is None else _DTYPE[dtype_out], steps,
+        0 if g is None else g.data_ptr(), cols if ldg is None else ldg,
+        0 if out is None else out.data_ptr(), cols if ldo is None else ldo,
+        ctypes.addressof(values), eps, scale)
+    a.keep = values  # the struct holds only their address
+    return a
+
+
+def newton_schulz(g, out, workspace=None, stream=None, **kw):
+    """Enqueue out = the orthogonalised update ``g`` on ``stream``: ``steps``
+    Newton-Schulz steps from g / (|g| + eps), times ``scale``."""
+    args = newton_schulz_args(g, out, **kw)
+    if workspace is not None:
+        skg_run_newton_schulz(args, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _handle(stream))
+        return
+    need = skg_newton_schulz_workspace_bytes(args)
+    if not need:
+        skg_run_newton_schulz(args, 0, 0, _handle(stream))
+        return
+    import torch
+    with _pool_of(stream):
+        ws = torch.empty(need, dtype=torch.uint8, device=out.device)
+    skg_run_newton_schulz(args, ws.data_ptr(), need, _handle(stream))

@@ -13,7 +13,7 @@ LIB_PATH = os.path.join(_HERE, "libskgemm.so")
 
 SKG_OK, SKG_ERR_HIP, SKG_ERR_UNSUPPORTED = 0, -1, -2
 F16, BF16, F8E4M3, F32, F8E5M2, F4E2M1 = 0, 1, 2, 3, 4, 5
-SCALE_ROWCOL, SCALE_TENSOR, SCALE_MX_E8M0 = 0, 1, 2
+SCALE_ROWCOL, SCALE_TENSOR, SCALE_MX_E8M0, SCALE_BLOCK128, SCALE_ROW128 = 0, 1, 2, 3, 4
 MODE_DP, MODE_DP_SK, MODE_PERSISTENT, MODE_SPLITK, MODE_AUTO = 0, 1, 2, 3, 4
 RED_LINEAR, RED_TREE, RED_ATOMIC, RED_WORKSPACE, RED_AUTO, RED_SCATTER = 0, 1, 2, 3, 4, 5
 OP_GEMM, OP_WGRAD, OP_FWD, OP_DGRAD = 0, 1, 2, 3
@@ -22,8 +22,9 @@ TILE_128x128x32, TILE_256x256x64, TILE_256x256x128, TILE_32x64x64, TILE_128x128x
     TILE_256x128x64, TILE_128x128x128, TILE_64x144x32, TILE_128x64x32, TILE_256x256x256, \
     TILE_128x128x256, TILE_16x16x512, TILE_16x32x512, \
     TILE_16x64x512, TILE_32x32x512, TILE_32x64x512, TILE_48x32x512, TILE_64x64x512, \
-    TILE_256x128x256 = range(19)
-TILE_COUNT = 19
+    TILE_256x128x256, TILE_16x16x128, TILE_16x32x128, TILE_32x32x128, TILE_32x64x128, \
+    TILE_64x64x128, TILE_256x128x128 = range(25)
+TILE_COUNT = 25
 
 MODES = {"dp": MODE_DP, "dp_sk": MODE_DP_SK, "persistent": MODE_PERSISTENT,
          "splitk": MODE_SPLITK, "auto": MODE_AUTO}
@@ -31,7 +32,12 @@ REDUCTIONS = {"linear": RED_LINEAR, "tree": RED_TREE, "atomic": RED_ATOMIC,
               "workspace": RED_WORKSPACE, "auto": RED_AUTO, "scatter": RED_SCATTER}
 DTYPES = {"f16": F16, "bf16": BF16, "e4m3": F8E4M3, "f32": F32, "e5m2": F8E5M2,
           "e2m1": F4E2M1}
-SCALE_MODES = {"rowcol": SCALE_ROWCOL, "tensor": SCALE_TENSOR, "mx": SCALE_MX_E8M0}
+SCALE_MODES = {"rowcol": SCALE_ROWCOL, "tensor": SCALE_TENSOR, "mx": SCALE_MX_E8M0,
+               "block128": SCALE_BLOCK128, "row128": SCALE_ROW128}
+BLOCK_1x128, BLOCK_128x128 = 0, 1
+BLOCKS = {"1x128": BLOCK_1x128, "128x128": BLOCK_128x128}
+ROPE_HALF, ROPE_PAIRS = 0, 1
+ROPE_STYLES = {"half": ROPE_HALF, "pairs": ROPE_PAIRS}
 SK_ORDER_AUTO, SK_ORDER_BLOCK, SK_ORDER_XCD, SK_ORDER_KMAJOR = 0, 1, 2, 3
 SK_ORDERS = {"auto": SK_ORDER_AUTO, "block": SK_ORDER_BLOCK, "xcd": SK_ORDER_XCD,
              "kmajor": SK_ORDER_KMAJOR}
@@ -43,7 +49,10 @@ TILES = {"128x128x32": TILE_128x128x32, "256x256x64": TILE_256x256x64,
          "128x128x256": TILE_128x128x256, "16x16x512": TILE_16x16x512, "16x32x512": TILE_16x32x512,
          "16x64x512": TILE_16x64x512, "32x32x512": TILE_32x32x512,
          "32x64x512": TILE_32x64x512, "48x32x512": TILE_48x32x512,
-         "64x64x512": TILE_64x64x512, "256x128x256": TILE_256x128x256}
+         "64x64x512": TILE_64x64x512, "256x128x256": TILE_256x128x256,
+         "16x16x128": TILE_16x16x128, "16x32x128": TILE_16x32x128, "32x32x128": TILE_32x32x128,
+         "32x64x128": TILE_32x64x128, "64x64x128": TILE_64x64x128,
+         "256x128x128": TILE_256x128x128}
 
 
 class skg_tile_info_t(ctypes.Structure):
@@ -113,6 +122,43 @@ class skg_mx_args_t(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("transpose", ctypes.c_int32)]
 
 
+class skg_block_quant_args_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kq", ctypes.c_int64),
+                ("kqt", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dtype_q", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("qt", ctypes.c_void_p), ("ldqt", ctypes.c_int64), ("scales_t", ctypes.c_void_p)]
+
+
+class skg_head_strides_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class skg_heads_args_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seq", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("heads_q", "heads_k", "head_dim", "rope_dim", "dtype",
+                                              "dtype_w", "style", "pos_bits")] + \
+               [("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_strides", skg_head_strides_t), ("k_strides", skg_head_strides_t),
+                ("yq", ctypes.c_void_p), ("yk", ctypes.c_void_p),
+                ("yq_strides", skg_head_strides_t), ("yk_strides", skg_head_strides_t),
+                ("weight_q", ctypes.c_void_p), ("weight_k", ctypes.c_void_p),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("pos0", ctypes.c_int64), ("dyq", ctypes.c_void_p), ("dyk", ctypes.c_void_p),
+                ("dyq_strides", skg_head_strides_t), ("dyk_strides", skg_head_strides_t),
+                ("dwq", ctypes.c_void_p), ("dwk", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class skg_newton_schulz_args_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dtype_out", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                ("coefficients", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
 class skg_plan_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("tm", "tn", "tk", "n_waves", "mode", "reduction")] + \
                [(n, ctypes.c_int64) for n in
@@ -176,7 +222,29 @@ EXPORTS = {
                                                 ctypes.POINTER(ctypes.c_int32)]),
     "skg_run_mx_quant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
     "skg_run_mx_dequant": (ctypes.c_int, [ctypes.POINTER(skg_mx_args_t), ctypes.c_void_p]),
+    "skg_run_block_quant": (ctypes.c_int, [ctypes.POINTER(skg_block_quant_args_t),
+                                           ctypes.c_void_p]),
+    "skg_run_qknorm_rope": (ctypes.c_int, [ctypes.POINTER(skg_heads_args_t), ctypes.c_void_p]),
+    "skg_qknorm_rope_bwd_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(skg_heads_args_t),
+                                                           ctypes.POINTER(ctypes.c_size_t)]),
+    "skg_run_qknorm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(skg_heads_args_t), ctypes.c_void_p,
+                                               ctypes.c_size_t, ctypes.c_void_p]),
+    "skg_plan_run_qknorm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(skg_heads_args_t),
+                                                    ctypes.c_void_p, ctypes.c_size_t,
+                                                    ctypes.c_void_p,
+                                                    ctypes.POINTER(ctypes.c_size_t),
+                                                    ctypes.POINTER(ctypes.c_int32)]),
+    "skg_newton_schulz_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(skg_newton_schulz_args_t),
+                                                         ctypes.POINTER(ctypes.c_size_t)]),
+    "skg_run_newton_schulz": (ctypes.c_int, [ctypes.POINTER(skg_newton_schulz_args_t),
+                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 }
+
+# Widest head of the head norms.
+HEADS_MAX_DIM = 512
+
+# Most steps of the Newton-Schulz products.
+NEWTON_SCHULZ_MAX_STEPS = 64
 
 # Longest row of the norm and its gradient.
 NORM_MAX_COLS = 32768
@@ -344,3 +412,39 @@ def skg_run_mx_quant(args, stream_ptr):
 
 def skg_run_mx_dequant(args, stream_ptr):
     return check(load().skg_run_mx_dequant(ctypes.byref(args), stream_ptr))
+
+
+def skg_run_block_quant(args, stream_ptr):
+    return check(load().skg_run_block_quant(ctypes.byref(args), stream_ptr))
+
+
+def skg_run_qknorm_rope(args, stream_ptr):
+    return check(load().skg_run_qknorm_rope(ctypes.byref(args), stream_ptr))
+
+
+def skg_qknorm_rope_bwd_workspace_bytes(args):
+    out = ctypes.c_size_t()
+    check(load().skg_qknorm_rope_bwd_workspace_bytes(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def skg_run_qknorm_rope_bwd(args, ws_ptr, ws_bytes, stream_ptr):
+    return check(load().skg_run_qknorm_rope_bwd(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))
+
+
+def skg_plan_run_qknorm_rope_bwd(args, ws_ptr, ws_bytes, stream_ptr):
+    """(bytes of workspace that the call takes, whether it was launched)."""
+    need, launched = ctypes.c_size_t(), ctypes.c_int32()
+    check(load().skg_plan_run_qknorm_rope_bwd(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr,
+                                              ctypes.byref(need), ctypes.byref(launched)))
+    return need.value, launched.value
+
+
+def skg_newton_schulz_workspace_bytes(args):
+    out = ctypes.c_size_t()
+    check(load().skg_newton_schulz_workspace_bytes(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def skg_run_newton_schulz(args, ws_ptr, ws_bytes, stream_ptr):
+    return check(load().skg_run_newton_schulz(ctypes.byref(args), ws_ptr, ws_bytes, stream_ptr))

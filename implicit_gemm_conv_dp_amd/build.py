@@ -31,7 +31,8 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["skg_host.cpp", "skg_api.hip", "skg_inst_gemm.hip", "skg_inst_gemm_f16.hip",
            "skg_inst_gemm_bf16.hip", "skg_inst_gemm_f8.hip", "skg_inst_gemm_f4.hip",
            "skg_inst_wgrad.hip", "skg_inst_fwd.hip", "skg_inst_dgrad.hip", "skg_norm.hip",
-           "skg_mx.hip"]
+           "skg_mx.hip", "skg_inst_gemm_f8_block.hip", "skg_block.hip", "skg_heads.hip",
+           "skg_newton.hip"]
 
 
 def _compile(src):

@@ -55,21 +55,27 @@ int current_device(DeviceRec* out) {
 }
 
 // CU count and resident CTAs per CU of one instance on the current device.
-int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
+// scale_mode: of a GEMM; -1 for the one that the tile and type come with.
+int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu, int scale_mode = -1) {
   DeviceRec d;
   int rc = current_device(&d);
   if (rc) return rc;
   if (!d.gfx950) return unsupported(std::string("unsupported arch ") + d.arch + " (the engine is built for gfx950)");
   // The runtime's answer for an instance does not change: asked for once.
+  if (op == SKG_OP_GEMM && !block_scales(scale_mode)) {
+    const TileDesc* t = tile_desc(tile_id);
+    const bool f8 = dtype == SKG_F8E4M3 || dtype == SKG_F8E5M2;
+    scale_mode = dtype == SKG_F4E2M1 ? SKG_SCALE_MX_E8M0 : f8 && t && t->dp_only ? SKG_SCALE_BLOCK128 : SKG_SCALE_ROWCOL;
+  }
   struct Known {
-    int op, tile, dtype, occ;
+    int op, tile, dtype, scale_mode, occ;
   };
   static std::mutex mu;
   static std::vector<Known> known;
   {
     std::lock_guard<std::mutex> lk(mu);
     for (const Known& k : known)
-      if (k.op == op && k.tile == tile_id && k.dtype == dtype) {
+      if (k.op == op && k.tile == tile_id && k.dtype == dtype && k.scale_mode == scale_mode) {
         *cus = d.cus;
         *per_cu = k.occ;
         return SKG_OK;
@@ -78,7 +84,7 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   int occ = 0;
   hipError_t e;
   if (op == SKG_OP_GEMM) {
-    GemmInst in = gemm_instance(tile_id, dtype, dtype == SKG_F4E2M1 ? SKG_SCALE_MX_E8M0 : SKG_SCALE_ROWCOL);
+    GemmInst in = gemm_instance(tile_id, dtype, scale_mode);
     if (!in.occupancy) return unsupported("no GEMM instance for this tile and dtype");
     e = in.occupancy(&occ);
   } else if (op == SKG_OP_WGRAD) {
@@ -96,7 +102,7 @@ int device_capacity(int op, int tile_id, int dtype, int* cus, int* per_cu) {
   if (occ <= 0) return unsupported("kernel instance cannot be resident on this device");
   {
     std::lock_guard<std::mutex> lk(mu);
-    known.push_back({op, tile_id, dtype, occ});
+    known.push_back({op, tile_id, dtype, scale_mode, occ});
   }
   *cus = d.cus;
   *per_cu = occ;
@@ -487,6 +493,18 @@ int run_conv(const skg_conv_args_t* a, bool dgrad, void* ws, size_t ws_bytes, hi
   return SKG_OK;
 }
 
+// The plan of a GEMM.  With a scale for each 128 of K auto is dp: nothing is
+// split, and the tiles of the ring kernels are eight waves'.
+int plan_gemm(const skg_gemm_args_t* a, const TileDesc& t, int cus, int per_cu, skg_plan_t* out) {
+  const bool block = block_scales(a->scale_mode);
+  const int mode = block && a->mode == SKG_MODE_AUTO ? SKG_MODE_DP : a->mode;
+  const int rc = plan_launch(gemm_shape(a, t), t, mode, a->reduction, a->ctas, resolve_sk_order(a->sk_order, false), cus, per_cu, out);
+  if (rc) return rc;
+  out->requested_mode = a->mode;
+  if (block && t.tm >= 128) out->n_waves = 8;
+  return SKG_OK;
+}
+
 // out, launched: the plan is wanted, and a workspace too small for it is not
 // an error but leaves the call undone.
 int run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream, skg_plan_t* out, int32_t* launched) {
@@ -502,14 +520,15 @@ int run_gemm(const skg_gemm_args_t* args, void* ws, size_t ws_bytes, void* strea
   const TileDesc* t = tile_desc(a->tile_id);
   if (a->scale_mode == SKG_SCALE_MX_E8M0 && (!a->scale_a || !a->scale_b))
     return unsupported("MX block scales need both scale arrays");
+  if (block_scales(a->scale_mode) && (!a->scale_a || !a->scale_b))
+    return unsupported("a scale for each 128 of K needs both scale arrays");
   GemmInst inst = gemm_instance(a->tile_id, a->dtype_ab, a->scale_mode);
   if (!inst.launch) return unsupported("no GEMM instance for this tile and dtype");
   int cus = 0, per_cu = 0;
-  rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu);
+  rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu, a->scale_mode);
   if (rc) return rc;
   skg_plan_t pl;
-  rc = plan_launch(gemm_shape(a, *t), *t, a->mode, a->reduction, a->ctas,
-                   resolve_sk_order(a->sk_order, false), cus, per_cu, &pl);
+  rc = plan_gemm(a, *t, cus, per_cu, &pl);
   if (rc) return rc;
   if (out) *out = pl;
   if (launched) {
@@ -607,11 +626,10 @@ int skg_plan_gemm(const skg_gemm_args_t* args, skg_plan_t* out) {
     const TileDesc* t = tile_desc(a->tile_id);
     int cus = 0, per_cu = 0;
     if (a->ctas == -1) {
-      rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu);
+      rc = device_capacity(SKG_OP_GEMM, a->tile_id, a->dtype_ab, &cus, &per_cu, a->scale_mode);
       if (rc) return rc;
     }
-    return plan_launch(gemm_shape(a, *t), *t, a->mode, a->reduction, a->ctas,
-                       resolve_sk_order(a->sk_order, false), cus, per_cu, out);
+    return plan_gemm(a, *t, cus, per_cu, out);
   } catch (...) {
     return hip_failure("exception in skg_plan_gemm");
   }

@@ -47,6 +47,12 @@ const TileDesc kTiles[SKG_TILE_COUNT] = {
     /* 48x32x512 */ {48, 32, 512, 4, M_F4, 0, 0, 0, true},
     /* 64x64x512 */ {64, 64, 512, 4, M_F4, 0, 0, 0, true},
     /* 256x128x256 */ {256, 128, 256, 4, M_F4, 0, 0, 0, true},
+    /* 16x16x128 */ {16, 16, 128, 4, M_F8, 0, 0, 0, true},
+    /* 16x32x128 */ {16, 32, 128, 4, M_F8, 0, 0, 0, true},
+    /* 32x32x128 */ {32, 32, 128, 4, M_F8, 0, 0, 0, true},
+    /* 32x64x128 */ {32, 64, 128, 4, M_F8, 0, 0, 0, true},
+    /* 64x64x128 */ {64, 64, 128, 4, M_F8, 0, 0, 0, true},
+    /* 256x128x128 */ {256, 128, 128, 4, M_F8, 0, 0, 0, true},
 };
 
 // Offsets inside one buffer are 32-bit on the device (buffer resources).
@@ -163,7 +169,7 @@ int plan_launch(const GemmShape& g, const TileDesc& t, int mode, int reduction, 
     return unsupported("this tile runs whole tiles a workgroup: mode dp or auto");
   // fp4: the dp kernels are ahead of every split over the whole sweep of
   // resolve_gemm (1500x1500x4096 15.9 us against 30.3 on stream-K).
-  if ((t.gemm_mask & M_F4) && mode == SKG_MODE_AUTO) mode = SKG_MODE_DP;
+  if ((t.dp_only || (t.gemm_mask & M_F4)) && mode == SKG_MODE_AUTO) mode = SKG_MODE_DP;
   int rc = resolve_launch(g, mode, reduction, ctas, num_cus, resident_per_cu, slices);
   if (rc) return rc;
   rc = make_plan(g, t, mode, reduction, ctas, num_cus, resident_per_cu, out);
@@ -361,8 +367,14 @@ static bool spans_rows(const TileDesc& t, const skg_gemm_args_t* a) {
 //   256x256), 4096x4096x4096 39.9 on 256x256 (45.6 on 256x128, 50.4 on
 //   128x128), 7349x2145x4224 52.2 on 256x128 (56.9 on 128x128, 73.7 on
 //   256x256).
+static int resolve_block_tile(const skg_gemm_args_t& r);
+
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   skg_gemm_args_t r = *a;
+  if (block_scales(r.scale_mode)) {
+    if (r.tile_id == SKG_TILE_AUTO) r.tile_id = resolve_block_tile(r);
+    return r;
+  }
   if (r.tile_id != SKG_TILE_AUTO || r.dtype_ab != SKG_F4E2M1) return r;
   r.tile_id = SKG_TILE_128x128x256;  // until a better one is found; also for sizes that are refused
   if (r.M <= 0 || r.N <= 0 || r.K <= 0) return r;
@@ -392,6 +404,12 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   return r;
 }
 
+// The tile of an 8-bit product with a scale for each 128 of K.
+static int resolve_block_tile(const skg_gemm_args_t& r) {
+  if (r.M <= 0 || r.N <= 0 || r.K <= 0) return SKG_TILE_64x64x128;
+  return SKG_TILE_64x64x128;
+}
+
 int validate_gemm(const skg_gemm_args_t* a) {
   if (!a) return unsupported("null arguments");
   const TileDesc* t = tile_desc(a->tile_id);
@@ -400,8 +418,20 @@ int validate_gemm(const skg_gemm_args_t* a) {
       a->dtype_ab != SKG_F8E5M2 && a->dtype_ab != SKG_F4E2M1)
     return unsupported("unsupported A/B dtype");
   if (a->scale_mode != SKG_SCALE_ROWCOL && a->scale_mode != SKG_SCALE_TENSOR &&
-      a->scale_mode != SKG_SCALE_MX_E8M0)
+      a->scale_mode != SKG_SCALE_MX_E8M0 && !block_scales(a->scale_mode))
     return unsupported("unknown scale mode");
+  if (block_scales(a->scale_mode)) {
+    if (a->dtype_ab != SKG_F8E4M3 && a->dtype_ab != SKG_F8E5M2)
+      return unsupported("this scale mode, a scale for each 128 of K, needs fp8 or bf8 inputs");
+    if (a->K % 128) return unsupported("a scale for each 128 of K needs K to be a multiple of 128");
+    if (a->mode != SKG_MODE_DP && a->mode != SKG_MODE_AUTO)
+      return unsupported("a scale for each 128 of K runs whole tiles a workgroup: mode dp or auto");
+    if (a->M > INT32_MAX - 255 || a->N > INT32_MAX - 255 || a->ldc > INT32_MAX) return unsupported("dimension too large");
+    if (a->M > 0 && a->N > 0 && a->K / 128 * 4 > kMaxBufferBytes / std::max(a->M, a->N))
+      return unsupported("scale array too large for 32-bit offsets");
+  } else if (t->dp_only && (t->gemm_mask & M_F8)) {
+    return unsupported("this tile needs a scale for each 128 of K");
+  }
   if (a->scale_mode == SKG_SCALE_MX_E8M0) {
     if (a->dtype_ab == SKG_F4E2M1) {
       if (!(t->gemm_mask & M_F4)) return unsupported("fp4 inputs need an fp4 tile");

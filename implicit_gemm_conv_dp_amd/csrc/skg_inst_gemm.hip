@@ -7,6 +7,8 @@ namespace skg {
 
 GemmInst gemm_instance(int tile_id, int dtype, int scale_mode) {
   const bool tensor = scale_mode == SKG_SCALE_TENSOR;
+  if (scale_mode == SKG_SCALE_BLOCK128 || scale_mode == SKG_SCALE_ROW128)
+    return gemm_instance_f8_block(tile_id, dtype, scale_mode == SKG_SCALE_ROW128);
   switch (dtype) {
     case SKG_F16: return scale_mode == SKG_SCALE_MX_E8M0 ? GemmInst{nullptr, nullptr} : gemm_instance_f16(tile_id, tensor);
     case SKG_BF16: return scale_mode == SKG_SCALE_MX_E8M0 ? GemmInst{nullptr, nullptr} : gemm_instance_bf16(tile_id, tensor);

@@ -50,6 +50,9 @@ inline bool whole_slices(const skg_plan_t& p) {
          p.sk_ctas == p.sk_tiles * (p.iters_per_tile / p.iters_per_sk_cta);
 }
 
+// A scale mode of one fp32 scale for each 128 of K.
+inline bool block_scales(int scale_mode) { return scale_mode == SKG_SCALE_BLOCK128 || scale_mode == SKG_SCALE_ROW128; }
+
 // Bits of one element, and bytes of n of them (n * bits a multiple of 8).
 int elem_bits(int dtype);
 inline int64_t row_bytes(int dtype, int64_t n) { return n * elem_bits(dtype) / 8; }

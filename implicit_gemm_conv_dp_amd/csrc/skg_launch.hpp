@@ -33,6 +33,8 @@ GemmInst gemm_instance_f16(int tile_id, bool tensor_scales);
 GemmInst gemm_instance_bf16(int tile_id, bool tensor_scales);
 GemmInst gemm_instance_f8(int tile_id, int dtype, int scale_mode);
 GemmInst gemm_instance_f4(int tile_id);
+// An fp32 scale for each 128 of K; rows: for each column of B too.
+GemmInst gemm_instance_f8_block(int tile_id, int dtype, bool rows);
 WgradInst wgrad_instance(int tile_id, int dtype);
 ConvInst fwd_instance(int tile_id, int dtype);
 ConvInst dgrad_instance(int tile_id, int dtype);

@@ -174,6 +174,20 @@ SKG_DEV typename Op::T group_reduce(typename Op::T v, SKG_LDS uint32_t* slot) {
   return v;
 }
 
+// 1 / sqrt(v) within half an ulp or so: the hardware's reciprocal square
+// root and one Newton step.  A subnormal v, which the instruction takes for
+// zero, is scaled by an even power of two.  Infinite for a zero, 0 for an
+// infinite v, NaN for a NaN.
+SKG_DEV float rsqrt_refined(float v) {
+  const bool small = v < 0x1p-126f;
+  const float u = small ? v * 0x1p+64f : v;
+  const float r = __builtin_amdgcn_rsqf(u);
+  const float e = __builtin_fmaf(-u * r, r, 1.f);
+  const float n = __builtin_fmaf(0.5f * r, e, r);
+  const float f = u > 0.f && u < 3e38f ? n : r;
+  return small ? f * 0x1p+32f : f;
+}
+
 // --- MX codes ------------------------------------------------------------------
 // E8M0 code of a block whose largest magnitude has the bits `top`: the
 // exponent of that magnitude less the format's largest one (2 for e2m1, 8

@@ -1,0 +1,468 @@
+// Orthogonalisation of an update by Newton-Schulz products (as the Muon optimiser
+// does): X = G / (|G|_F + eps), then steps times
+//   S = X X^T,   P = b S + c S^2,   X <- a X + P X.
+//
+// X is m x n with m <= n (G, or G transposed).  It is kept both ways in the
+// workspace, X (m x n) and Y = X^T (n x m): S reduces over n, where X's rows are
+// contiguous, and Y <- a Y + Y P over m, where Y's and the symmetric P's are; so
+// every product is of two operands whose rows run along K, and a tile is written
+// as it is and transposed.  S and P are symmetric: only tiles on and below the
+// diagonal are computed, and written twice.
+//
+// Between the products everything is fp16 times a power of two (X 2^13, S 2^12,
+// P 2^11): eleven bits against bf16's eight at the same rate of the matrix
+// instructions, and S of a large matrix, whose entries are around 1/m, stays clear
+// of fp16's subnormals.  Sums, the polynomial and the update are fp32, each
+// rounded once when it is stored; the norm's sum is fp64.
+//
+// Rows in the workspace are padded to whole 128 bytes with zeros: a product of
+// padded operands is zero there, so the copy-out keeps the padding zero by writing
+// it like the rest.
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <string>
+
+#include "skg_internal.hpp"
+#include "skg_lowp.hpp"
+#include "skg_ring8.hpp"
+
+namespace skg {
+namespace {
+
+constexpr float kScaleX = 0x1p+13f, kScaleS = 0x1p+12f, kScaleP = 0x1p+11f;
+
+// C = alpha A B^T + beta D: A M x K, B N x K, D and C M x N, Ct N x M, fp16 with
+// rows of whole 128 bytes (the last step's C or Ct: the caller's type).
+struct NsParams {
+  const char *A, *B;
+  const char* D;  // or nullptr; C's layout
+  char *C, *Ct;   // either may be nullptr
+  int M, N, K;
+  int cn, ctn;               // columns of C and Ct that are written
+  uint32_t lda_b, ldb_b;     // bytes
+  int64_t ldd, ldc, ldct;    // elements
+  float alpha, beta;
+  int dt;                    // of C and Ct: DT_F16, DT_BF16 or DT_F32
+  int vec;                   // C and Ct are aligned to 16 bytes
+  int sym;                   // M == N: tiles on and below the diagonal; Ct is C
+  int tiles_m, tiles_n, tiles;
+};
+
+// Tile `id` of the list: rows and columns in tiles.  Full grids are walked in
+// strips of four tile rows, column by column, so that neighbours share operands.
+SKG_DEV void ns_tile(const NsParams& p, int id, int& tm, int& tn) {
+  if (p.sym) {
+    tm = (int)((__builtin_sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+    while (tm * (tm + 1) / 2 > id) --tm;
+    while ((tm + 1) * (tm + 2) / 2 <= id) ++tm;
+    tn = id - tm * (tm + 1) / 2;
+  } else {
+    constexpr int G = 4;
+    const int strip = id / (G * p.tiles_n), in = id - strip * G * p.tiles_n, rows = min(G, p.tiles_m - strip * G);
+    tn = in / rows;
+    tm = strip * G + in - tn * rows;
+  }
+}
+
+template <int DT>
+SKG_DEV uint32_t ns_pack(float a, float b) {
+  return DT == DT_F16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+}
+SKG_DEV float half_at(const i32x4& v, int i) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)((uint32_t)v[i >> 1] >> (16 * (i & 1))));
+}
+
+// --- few tiles -------------------------------------------------------------------
+// Four waves split K, each streaming its part through LDS of its own, D stages of
+// 64 elements ahead; the partial tiles are added in a fixed order.
+template <int FM, int FN, int D>
+struct NsDirect {
+  static constexpr int TM = 16 * FM, TN = 16 * FN, WAVES = 4, RB = 128;
+  static constexpr int UA = TM / 8, UB = TN / 8, PER = UA + UB, SLOT = (TM + TN) * RB;
+  static constexpr int WAVE_LDS = D * SLOT, RED = WAVES * FM * FN * 64 * 16;
+  static constexpr int LDS = WAVES * WAVE_LDS > RED ? WAVES * WAVE_LDS : RED;
+  static_assert(LDS <= 160 * 1024, "tile");
+
+  SKG_DEV static void run(const NsParams& g, SKG_LDS char* group_lds) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    SKG_LDS char* lds = group_lds + wave * WAVE_LDS;
+    const TileRun run(g.tiles);
+    int tm, tn;
+    ns_tile(g, run.first + run.k, tm, tn);
+    const int m0 = tm * TM, n0 = tn * TN, stages = (g.K + 63) / 64;
+    int na, nb;
+    const i32x4 ra = ring_rows(g.A, m0, g.M, g.lda_b, g.lda_b, na), rb = ring_rows(g.B, n0, g.N, g.ldb_b, g.ldb_b, nb);
+    uint32_t offa[2], offb[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      int row, chunk;
+      lds_slot<RB>(n * 64 + lane, row, chunk);
+      offa[n] = (uint32_t)(row - 8 * n) * g.lda_b + chunk * 16;
+      offb[n] = (uint32_t)(row - 8 * n) * g.ldb_b + chunk * 16;
+    }
+    const int first = (int)((int64_t)stages * wave / WAVES), count = (int)((int64_t)stages * (wave + 1) / WAVES) - first;
+    auto issue = [&](int s, int at) {
+      const bool live = s < count;
+      const uint32_t kb = live ? (uint32_t)(first + s) * RB : 0, dst = lds_addr(lds) + at * SLOT;
+      i32x4 a = ra, b = rb;
+      a[2] = live ? na : 0;
+      b[2] = live ? nb : 0;
+      static_for<0, UB>([&](auto n_) {
+        constexpr int n = decltype(n_)::value;
+        ring_dma16<TM * RB + n * 1024>(b, dst, offb[n & 1] + n * 8 * g.ldb_b, kb);
+      });
+      static_for<0, UA>([&](auto n_) {
+        constexpr int n = decltype(n_)::value;
+        ring_dma16<n * 1024>(a, dst, offa[n & 1] + n * 8 * g.lda_b, kb);
+      });
+    };
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](int at) {
+      const SKG_LDS char* st = lds + at * SLOT;
+      const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        i32x4 a[FM], b[FN];
+#pragma unroll
+        for (int f = 0; f < FM; ++f) a[f] = *(const SKG_LDS i32x4*)(st + lds_off<RB>(f * 16 + r, k * 4 + q));
+#pragma unroll
+        for (int f = 0; f < FN; ++f) b[f] = *(const SKG_LDS i32x4*)(st + TM * RB + lds_off<RB>(f * 16 + r, k * 4 + q));
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) Mfma<DT_F16, 16>::run(acc[i][j], b[j], a[i]);
+      }
+    };
+    if (count > 0) {
+      static_for<0, D>([&](auto s_) { issue(decltype(s_)::value, decltype(s_)::value); });
+      for (int s = 0; s < count; s += D) {
+        static_for<0, D>([&](auto d_) {
+          constexpr int d = decltype(d_)::value;
+          if (s + d < count) {
+            wait_vm<(D - 1) * PER>();
+            compute(d);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue(s + d + D, d);
+          }
+        });
+      }
+      wait_vm<0>();
+    }
+    __syncthreads();  // LDS becomes the partial tiles'
+    SKG_LDS f32x4* red = (SKG_LDS f32x4*)group_lds;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) red[(wave * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < (FM * FN + WAVES - 1) / WAVES; ++k) {
+      const int f = k * WAVES + wave;
+      if (f >= FM * FN) break;
+      f32x4 v = red[f * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v += red[(w * FM * FN + f) * 64 + lane];
+      const int m = m0 + f / FN * 16 + (lane & 15), n = n0 + f % FN * 16 + 4 * (lane >> 4);
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (g.D && m < g.M && n < g.cn) {  // D's rows are padded: whole fours
+        const uint2 d = *(const uint2*)(g.D + ((int64_t)m * g.ldd + n) * 2);
+        const i32x4 w = {(int)d.x, (int)d.y, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = half_at(w, e);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(v[e], g.alpha, x[e] * g.beta);
+      auto put = [&](char* base, int64_t at, float y) {
+        if (g.dt == DT_F32)
+          ((float*)base)[at] = y;
+        else
+          ((uint16_t*)base)[at] = g.dt == DT_F16 ? to_f16_bits(y) : to_bf16_bits(y);
+      };
+      if (g.C && m < g.M) {
+        if (g.vec && n + 4 <= g.cn) {
+          const int64_t at = (int64_t)m * g.ldc + n;
+          if (g.dt == DT_F32)
+            *(f32x4*)((float*)g.C + at) = f32x4{x[0], x[1], x[2], x[3]};
+          else
+            *(uint2*)((uint16_t*)g.C + at) = g.dt == DT_F16 ? make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]))
+                                                            : make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < g.cn) put(g.C, (int64_t)m * g.ldc + n + e, x[e]);
+        }
+      }
+      if (g.Ct && m < g.ctn && !(g.sym && tm == tn)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) put(g.Ct, (int64_t)(n + e) * g.ldct + m, x[e]);
+      }
+    }
+  }
+};
+template <class T>
+__global__ __launch_bounds__(256) void ns_direct_kernel(NsParams g) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
+  T::run(g, (SKG_LDS char*)lds);
+}
+
+// --- the norm and the operands' first form ---------------------------------------
+constexpr int kSumBlocks = 512;
+struct NsInput {
+  const char* g;
+  int64_t rows, cols, ldg;
+  double* partial;
+  char *x, *xt;      // G / norm as it lies (rows x cols) and transposed
+  int64_t px, pxt;   // their pitches in elements
+  float eps;
+  int blocks;
+};
+template <int DT>
+__global__ __launch_bounds__(256) void ns_sum_kernel(NsInput a) {
+  typedef typename Elem<DT>::raw raw;
+  __shared__ double part[4];
+  double sum = 0;
+  const raw* g = reinterpret_cast<const raw*>(a.g);
+  const uint32_t per = (uint32_t)((a.cols + 7) / 8);  // chunks a row
+  const int64_t all = a.rows * (int64_t)per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8, n = (int)min((int64_t)8, a.cols - c);
+    const raw* p = g + r * a.ldg + c;
+    if (n == 8) {
+      const Chunk<DT> v = reinterpret_cast<const Loose<Chunk<DT>>*>(p)->c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)v.get(j), (double)v.get(j), sum);
+    } else {
+      for (int j = 0; j < n; ++j) sum = __builtin_fma((double)Elem<DT>::get(p[j]), (double)Elem<DT>::get(p[j]), sum);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) a.partial[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+}
+// Tiles of 64 x 64: both forms, their padding with zeros.
+template <int DT>
+__global__ __launch_bounds__(256) void ns_first_kernel(NsInput a) {
+  typedef typename Elem<DT>::raw raw;
+  __shared__ double part[4];
+  __shared__ uint16_t tile[64][66];
+  double sum = 0;
+  for (int i = threadIdx.x; i < a.blocks; i += 256) sum += a.partial[i];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  const double f = (double)kScaleX / (__builtin_sqrt(part[0] + part[1] + part[2] + part[3]) + (double)a.eps);
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const raw* g = reinterpret_cast<const raw*>(a.g);
+  const int c = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < 64; i += 4) {
+    uint16_t h = 0;
+    if (r0 + i < a.rows && c0 + c < a.cols) h = to_f16_bits((float)((double)Elem<DT>::get(g[(r0 + i) * a.ldg + c0 + c]) * f));
+    tile[i][c] = h;
+    if (r0 + i < a.rows) reinterpret_cast<uint16_t*>(a.x)[(r0 + i) * a.px + c0 + c] = h;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x >> 6; i < 64; i += 4)
+    if (c0 + i < a.cols) reinterpret_cast<uint16_t*>(a.xt)[(c0 + i) * a.pxt + r0 + c] = tile[c][i];
+}
+
+// --- host ------------------------------------------------------------------------
+bool row_type(int dt) { return dt == SKG_F16 || dt == SKG_BF16 || dt == SKG_F32; }
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t pitch_of(int64_t n) { return ceil_div(n, 64) * 64; }
+
+// The workspace: partial sums, X and Y twice (a step reads one pair and writes the
+// other), S and P.
+struct NsSpace {
+  int64_t m, n, pm, pn;
+  size_t x[2], y[2], s, p, bytes;
+};
+NsSpace ns_space(const skg_newton_schulz_args_t* a) {
+  NsSpace w;
+  w.m = std::min(a->rows, a->cols);
+  w.n = std::max(a->rows, a->cols);
+  w.pm = pitch_of(w.m);
+  w.pn = pitch_of(w.n);
+  size_t at = kSumBlocks * sizeof(double);
+  auto take = [&](int64_t rows, int64_t pitch) {
+    const size_t r = at;
+    at += (size_t)rows * pitch * 2;  // whole 128-byte rows
+    return r;
+  };
+  for (int i = 0; i < 2; ++i) {
+    w.x[i] = take(w.m, w.pn);
+    w.y[i] = take(w.n, w.pm);
+  }
+  w.s = take(w.m, w.pm);
+  w.p = take(w.m, w.pm);
+  w.bytes = at;
+  return w;
+}
+
+int check_newton(const skg_newton_schulz_args_t* a) {
+  if (!a) return unsupported("null arguments");
+  if (!row_type(a->dtype) || !row_type(a->dtype_out)) return unsupported("the update is f16, bf16 or f32");
+  if (a->rows < 0 || a->cols < 0) return unsupported("rows and cols must not be negative");
+  // Rows of the fp16 operands within 32-bit offsets of a tile of 256.
+  constexpr int64_t most = (int64_t(INT32_MAX) / 256) / 2 - 64;
+  if (a->rows > most || a->cols > most) return unsupported("dimension too large");
+  if (a->steps < 1 || a->steps > SKG_NEWTON_SCHULZ_MAX_STEPS) return unsupported("steps must be 1 to SKG_NEWTON_SCHULZ_MAX_STEPS");
+  if (a->ldg < a->cols || a->ldo < a->cols) return unsupported("leading dimension too small");
+  if (!(a->eps >= 0.f)) return unsupported("eps must not be negative");
+  if (!std::isfinite(a->scale)) return unsupported("scale must be finite");
+  return SKG_OK;
+}
+
+hipError_t ns_product(NsParams p, hipStream_t st) {
+  typedef NsDirect<4, 4, 2> T;
+  p.tiles_m = (int)ceil_div(p.M, T::TM);
+  p.tiles_n = (int)ceil_div(p.N, T::TN);
+  p.tiles = p.sym ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL((ns_direct_kernel<T>), dim3((unsigned)p.tiles), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hipStream_t st) {
+  int rc = check_newton(a);
+  if (rc) return rc;
+  if (a->rows == 0 || a->cols == 0) return SKG_OK;
+  if (!a->g || !a->out || !a->coefficients) return unsupported("null g, out or coefficients");
+  for (int i = 0; i < 3 * a->steps; ++i)
+    if (!std::isfinite(a->coefficients[i])) return unsupported("coefficients must be finite");
+  if (!aligned_to(a->g, elem_bytes(a->dtype)) || !aligned_to(a->out, elem_bytes(a->dtype_out)))
+    return unsupported("pointers must be aligned to their elements");
+  const NsSpace w = ns_space(a);
+  if (w.bytes > ws_bytes) return unsupported("workspace too small for this call");
+  if (!ws || !aligned_to(ws, 256)) return unsupported("workspace must be 256-byte aligned device memory");
+  int cus = 0;
+  rc = check_device(&cus);
+  if (rc) return rc;
+  char* base = static_cast<char*>(ws);
+  const bool wide = a->rows <= a->cols;
+  NsInput in;
+  in.g = static_cast<const char*>(a->g);
+  in.rows = a->rows;
+  in.cols = a->cols;
+  in.ldg = a->ldg;
+  in.partial = reinterpret_cast<double*>(base);
+  in.x = base + (wide ? w.x[0] : w.y[0]);
+  in.xt = base + (wide ? w.y[0] : w.x[0]);
+  in.px = wide ? w.pn : w.pm;
+  in.pxt = wide ? w.pm : w.pn;
+  in.eps = a->eps;
+  in.blocks = (int)std::min<int64_t>(kSumBlocks, ceil_div(a->rows * ceil_div(a->cols, 8), 256));
+  auto first = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    hipLaunchKernelGGL((ns_sum_kernel<DT>), dim3((unsigned)in.blocks), dim3(256), 0, st, in);
+    hipLaunchKernelGGL((ns_first_kernel<DT>), dim3((unsigned)ceil_div(a->cols, 64), (unsigned)ceil_div(a->rows, 64)), dim3(256), 0, st, in);
+  };
+  if (a->dtype == SKG_F16)
+    first(std::integral_constant<int, DT_F16>{});
+  else if (a->dtype == SKG_BF16)
+    first(std::integral_constant<int, DT_BF16>{});
+  else
+    first(std::integral_constant<int, DT_F32>{});
+  hipError_t e = hipGetLastError();
+  const int m = (int)w.m, n = (int)w.n;
+  for (int i = 0; i < a->steps && e == hipSuccess; ++i) {
+    const float ca = a->coefficients[3 * i], cb = a->coefficients[3 * i + 1], cc = a->coefficients[3 * i + 2];
+    char *x = base + w.x[i & 1], *y = base + w.y[i & 1], *s = base + w.s, *poly = base + w.p;
+    NsParams p{};
+    p.dt = DT_F16;
+    p.vec = 1;
+    // S = X X^T
+    p.A = p.B = x;
+    p.lda_b = p.ldb_b = (uint32_t)w.pn * 2;
+    p.M = p.N = m;
+    p.K = n;
+    p.C = p.Ct = s;
+    p.ldc = p.ldct = w.pm;
+    p.cn = p.ctn = (int)w.pm;
+    p.alpha = kScaleS / (kScaleX * kScaleX);
+    p.sym = 1;
+    e = ns_product(p, st);
+    // P = b S + c S S
+    p.A = p.B = p.D = s;
+    p.lda_b = p.ldb_b = (uint32_t)w.pm * 2;
+    p.ldd = w.pm;
+    p.K = m;
+    p.C = p.Ct = poly;
+    p.alpha = cc * (kScaleP / (kScaleS * kScaleS));
+    p.beta = cb * (kScaleP / kScaleS);
+    if (e == hipSuccess) e = ns_product(p, st);
+    // Y <- a Y + Y P, and X
+    const bool last = i + 1 == a->steps;
+    p.A = p.D = y;
+    p.B = poly;
+    p.M = n;
+    p.N = m;
+    p.sym = 0;
+    p.ldd = w.pm;
+    p.C = base + w.y[1 - (i & 1)];
+    p.ldc = w.pm;
+    p.cn = (int)w.pm;
+    p.Ct = base + w.x[1 - (i & 1)];
+    p.ldct = w.pn;
+    p.ctn = (int)w.pn;
+    p.alpha = 1.f / kScaleP;
+    p.beta = ca;
+    if (last) {
+      p.dt = a->dtype_out == SKG_F32 ? DT_F32 : a->dtype_out == SKG_F16 ? DT_F16 : DT_BF16;
+      const int64_t es = elem_bytes(a->dtype_out);
+      p.vec = aligned_to(a->out, 16) && a->ldo * es % 16 == 0;
+      char* out = static_cast<char*>(a->out);
+      p.C = wide ? nullptr : out;
+      p.Ct = wide ? out : nullptr;
+      p.ldc = p.ldct = a->ldo;
+      p.cn = m;
+      p.ctn = n;
+      p.alpha *= a->scale / kScaleX;
+      p.beta *= a->scale / kScaleX;
+    }
+    if (e == hipSuccess) e = ns_product(p, st);
+  }
+  if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
+  return SKG_OK;
+}
+
+}  // namespace
+}  // namespace skg
+
+using namespace skg;
+
+extern "C" {
+
+int skg_newton_schulz_workspace_bytes(const skg_newton_schulz_args_t* a, size_t* out) {
+  try {
+    clear_error();
+    const int rc = check_newton(a);
+    if (rc) return rc;
+    if (!out) return unsupported("null output");
+    *out = a->rows == 0 || a->cols == 0 ? 0 : ns_space(a).bytes;
+    return SKG_OK;
+  } catch (...) {
+    return hip_failure("exception in skg_newton_schulz_workspace_bytes");
+  }
+}
+
+int skg_run_newton_schulz(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    clear_error();
+    return run_newton(a, ws, ws_bytes, static_cast<hipStream_t>(stream));
+  } catch (const std::exception& ex) {
+    return hip_failure(std::string("exception: ") + ex.what());
+  } catch (...) {
+    return hip_failure("unknown exception");
+  }
+}
+
+}  // extern "C"

@@ -96,7 +96,20 @@ enum skg_scale_mode {
    *                    with one of the fp4 tiles; K a multiple of 128, both
    *                    pointers non-NULL and 16-byte aligned; no further
    *                    scale. */
-  SKG_SCALE_MX_E8M0 = 2
+  SKG_SCALE_MX_E8M0 = 2,
+  /* An fp32 scale for each block of 128 consecutive K elements; fp8 or bf8
+   * inputs, K a multiple of 128, both pointers non-NULL:
+   *   C[m][n] = round(sum_b sa(b, m) sb(b, n) sum_{k in b} a(m,k) b(k,n)).
+   * scale_a holds K/128 lines of M floats: line b has block b's scale of every
+   * row of A.  With SKG_SCALE_ROW128 scale_b holds K/128 lines of N floats
+   * alike (both operands quantised along K, as a weight gradient's are); with
+   * SKG_SCALE_BLOCK128 one float stands for 128 consecutive columns too (K/128
+   * lines of ceil(N/128), as a weight's are).  These are the arrays that
+   * skg_run_block_quant writes.  Each array is at most 2^31 - 1 bytes.  Tiles:
+   * SKG_TILE_AUTO, 256x256x128, 128x128x128 and those of this mode alone; mode
+   * dp or auto (which is dp), no workspace. */
+  SKG_SCALE_BLOCK128 = 3,
+  SKG_SCALE_ROW128 = 4
 };
 
 /* Launch modes (PR #13151, Technical Details: Wgrad kernel, launch modes).
@@ -205,16 +218,20 @@ enum skg_sk_order {
 /* Compiled tile instances.  TM x TN x TK in elements; each instance exists
  * for the operations and input types skg_tile_info reports. */
 enum skg_tile {
-  /* fp4 GEMM only: the call picks the tile from M, N, K and the mode (the
-     plan's tm, tn and tk report it). */
+  /* fp4 GEMM and fp8 GEMM with a scale for each 128 only: the call picks the
+     tile from M, N, K and the mode (the plan's tm, tn and tk report it). */
   SKG_TILE_AUTO = -1,
   SKG_TILE_128x128x32 = 0,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x256x64 = 1,   /* f16/bf16 GEMM and wgrad, 4 waves */
-  SKG_TILE_256x256x128 = 2,  /* fp8 GEMM (also with MX block scales), 4 waves */
+  SKG_TILE_256x256x128 = 2,  /* fp8 GEMM (also with MX block scales), 4 waves;
+                                with a scale for each 128 of K, 8
+                                waves (the plan says so) */
   SKG_TILE_32x64x64 = 3,     /* f16/bf16 wgrad (small per-group M), 4 waves */
   SKG_TILE_128x128x64 = 4,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x128x64 = 5,   /* f16/bf16 GEMM and wgrad, 4 waves */
-  SKG_TILE_128x128x128 = 6,  /* fp8 GEMM (also with MX block scales), 4 waves */
+  SKG_TILE_128x128x128 = 6,  /* fp8 GEMM (also with MX block scales), 4 waves;
+                                with a scale for each 128 of K, 8
+                                waves (the plan says so) */
   SKG_TILE_64x144x32 = 7,    /* f16/bf16 grouped wgrad, block-diagonal: four whole
                                 groups of 16 input and 16 output channels per
                                 tile (GEMM-M = 64 output channels, GEMM-N = 9
@@ -238,7 +255,16 @@ enum skg_tile {
   SKG_TILE_48x32x512 = 16,
   SKG_TILE_64x64x512 = 17,
   SKG_TILE_256x128x256 = 18, /* fp4 GEMM with MX block scales, 4 waves; mode dp or auto */
-  SKG_TILE_COUNT = 19
+  /* fp8 GEMM with a scale for each 128 of K, for few tiles: 4 waves that split
+     the reduction; mode dp or auto, no workspace */
+  SKG_TILE_16x16x128 = 19,
+  SKG_TILE_16x32x128 = 20,
+  SKG_TILE_32x32x128 = 21,
+  SKG_TILE_32x64x128 = 22,
+  SKG_TILE_64x64x128 = 23,
+  SKG_TILE_256x128x128 = 24, /* the same scales, many tiles, 8 waves (the plan
+                                says so); mode dp or auto */
+  SKG_TILE_COUNT = 25
 };
 
 enum skg_op { SKG_OP_GEMM = 0, SKG_OP_WGRAD = 1, SKG_OP_FWD = 2, SKG_OP_DGRAD = 3 };
@@ -592,6 +618,136 @@ int skg_plan_run_rmsnorm_bwd(const skg_norm_bwd_args_t* args, void* ws, size_t w
                              size_t* need, int32_t* launched);
 int skg_run_mx_quant(const skg_mx_args_t* args, void* stream);
 int skg_run_mx_dequant(const skg_mx_args_t* args, void* stream);
+
+/* --- An 8-bit attention projection ---------------------------------------------
+ * What a projection of queries and keys needs around skg_run_gemm's products of
+ * 8-bit operands with a scale for each block of 128: the quantiser into such
+ * blocks, the norms of queries and keys for each head with the position's
+ * rotation, their gradient, and the orthogonalisation of the weight's update.
+ * As above, nothing here synchronises, allocates or uses a memset, so every call
+ * may be captured into a graph; zero rows or tokens are accepted and write
+ * nothing (gradients: dw = 0).  Calls that share a workspace must not overlap. */
+
+/* Quantisation into blocks of 128 elements along a row, of 128 x 128, or,
+ * transposed, of 128 along a column.  With top the largest magnitude of a block
+ * and MAX 448 (e4m3) or 57344 (e5m2): the scale is d = max(top / MAX, 2^-126) in
+ * fp32 and a code is the nearest to x MAX / top (to x / 2^-126 where d is that
+ * bound), the even one of two.  An infinity or NaN makes its block's scale and
+ * codes NaN.
+ *   q, scales     rows lines of kq codes, blocks along the rows: A or B of
+ *                 skg_run_gemm for a reduction over x's columns;
+ *   qt, scales_t  cols lines of kqt codes, blocks along the columns: the operand
+ *                 for a reduction over x's rows.
+ * Either may be NULL; both come from one read of x.  kq and kqt are multiples of
+ * 128 that cover their axis; codes past x's end are zero.  SKG_BLOCK_1x128:
+ * scales holds kq/128 lines of rows floats, scales_t kqt/128 lines of cols
+ * (SKG_SCALE_ROW128, and any A).  SKG_BLOCK_128x128: kq/128 lines of
+ * ceil(rows/128) and kqt/128 lines of ceil(cols/128) (B with
+ * SKG_SCALE_BLOCK128); q and qt then hold the same codes. */
+enum skg_block { SKG_BLOCK_1x128 = 0, SKG_BLOCK_128x128 = 1 };
+typedef struct skg_block_quant_args {
+  int64_t rows, cols;      /* of x */
+  int64_t kq, kqt;
+  int32_t dtype;           /* x: SKG_F16, SKG_BF16 or SKG_F32 */
+  int32_t dtype_q;         /* SKG_F8E4M3 or SKG_F8E5M2 */
+  int32_t block;           /* enum skg_block */
+  const void* x;
+  int64_t ldx;             /* elements */
+  void* q;
+  int64_t ldq;
+  float* scales;
+  void* qt;
+  int64_t ldqt;
+  float* scales_t;
+} skg_block_quant_args_t;
+int skg_run_block_quant(const skg_block_quant_args_t* args, void* stream);
+
+/* Widest head of the head norms. */
+#define SKG_HEADS_MAX_DIM 512
+
+/* Norms of queries and keys for each head with the position's rotation.  For
+ * each head of head_dim elements of each token:
+ *   s = 1 / sqrt(mean(x^2) + eps);  n = x s weight   (weight 1 when NULL);
+ *   y = n with its first rope_dim elements turned, pair i by the angle whose
+ *       cosine and sine are cos[p][i] and sin[p][i], p the token's position:
+ *       (a, b) -> (a cos - b sin, b cos + a sin).
+ * Pair i is (i, i + rope_dim/2) with SKG_ROPE_HALF and (2i, 2i + 1) with
+ * SKG_ROPE_PAIRS.  rope_dim may be 0: nothing is turned, the tables may be NULL.
+ * Everything is fp32 up to y's rounding.  positions holds batch x seq whole
+ * numbers of pos_bits bits, or is NULL: token t of each batch is at pos0 + t.  A
+ * position outside the table's table_rows rows gives NaN in the turned elements
+ * and reads nothing.
+ *
+ * The gradient: with g = dy turned back,
+ *   dx = s (g weight - x s^2 mean(g weight x));   dw = sum of g x s over tokens
+ *        and heads, fp32, in a fixed order.
+ * dx (yq, yk in the arguments) or dw may be NULL.  The workspace holds partial
+ * sums of dw; there is none without dw.
+ *
+ * Strides are in elements, between batches, tokens and heads; a head's elements
+ * are adjacent.  Results may be written over an input with the same strides.
+ * heads_q or heads_k may be 0: those pointers are then not looked at (gradient:
+ * dw = 0). */
+enum skg_rope_style { SKG_ROPE_HALF = 0, SKG_ROPE_PAIRS = 1 };
+typedef struct skg_head_strides {
+  int64_t batch, token, head;
+} skg_head_strides_t;
+typedef struct skg_heads_args {
+  int64_t batch, seq;
+  int32_t heads_q, heads_k, head_dim, rope_dim;
+  int32_t dtype;           /* q, k, yq, yk, dyq, dyk: SKG_F16, SKG_BF16 or SKG_F32 */
+  int32_t dtype_w;         /* weights: dtype or SKG_F32 */
+  int32_t style;           /* enum skg_rope_style */
+  int32_t pos_bits;        /* 32 or 64 */
+  const void *q, *k;
+  skg_head_strides_t q_strides, k_strides;
+  void *yq, *yk;           /* gradient: dq and dk */
+  skg_head_strides_t yq_strides, yk_strides;
+  const void *weight_q, *weight_k;  /* head_dim values each, or NULL */
+  const float *cos, *sin;  /* table_rows x rope_dim/2 */
+  int64_t table_rows;
+  const void* positions;
+  int64_t pos0;
+  const void *dyq, *dyk;   /* gradient only */
+  skg_head_strides_t dyq_strides, dyk_strides;
+  float *dwq, *dwk;
+  float eps;
+} skg_heads_args_t;
+int skg_run_qknorm_rope(const skg_heads_args_t* args, void* stream);
+int skg_qknorm_rope_bwd_workspace_bytes(const skg_heads_args_t* args, size_t* out);
+int skg_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t ws_bytes, void* stream);
+/* As skg_plan_run_rmsnorm_bwd. */
+int skg_plan_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t ws_bytes, void* stream,
+                                 size_t* need, int32_t* launched);
+
+/* Orthogonalisation of an update by Newton-Schulz products:
+ *   X = G / (|G|_F + eps);  steps times X <- a X + (b S + c S^2) X, S = X X^T;
+ *   out = scale X
+ * (S = X^T X on the other side where G has more rows than columns, which is the
+ * same).  coefficients holds a, b, c of each step (3 x steps host floats).  The
+ * norm is summed in fp64.  Between the products X and S are kept in fp16 with a
+ * fixed power of two each (2^13 and 2^12, the polynomial 2^11): ten or more
+ * binades below the largest entry keep their eleven bits, and entries of X up to
+ * 7, of S up to 15 and of b S + c S^2 up to 31 fit; coefficients that drive them
+ * further give infinities or NaN.  Sums are fp32.  dtype_out is SKG_BF16,
+ * SKG_F16 or SKG_F32 (the last is not rounded, but is no more exact than the
+ * fp16 factors make it).  G is read before out is written, so out may be G where
+ * their types and pitches agree.  A matrix without elements writes nothing. */
+#define SKG_NEWTON_SCHULZ_MAX_STEPS 64
+typedef struct skg_newton_schulz_args {
+  int64_t rows, cols;
+  int32_t dtype;           /* g: SKG_F16, SKG_BF16 or SKG_F32 */
+  int32_t dtype_out;
+  int32_t steps;
+  const void* g;
+  int64_t ldg;             /* elements */
+  void* out;
+  int64_t ldo;
+  const float* coefficients;
+  float eps, scale;
+} skg_newton_schulz_args_t;
+int skg_newton_schulz_workspace_bytes(const skg_newton_schulz_args_t* args, size_t* out);
+int skg_run_newton_schulz(const skg_newton_schulz_args_t* args, void* ws, size_t ws_bytes, void* stream);
 
 /* Timing hook for measurement: while set on the calling thread, every run
  * call records `start` (a hipEvent_t) on its stream immediately before the

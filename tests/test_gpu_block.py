@@ -1,0 +1,268 @@
+"""GPU parity of block quantisation and of the product of 8-bit operands with a
+scale for each block of 128, against float64.
+
+Quantisation: the scale is one fp32 division and has to be equal.  A code is a
+quotient rounded to fp32 and then to a code.  For bf16 and f16 inputs x MAX and
+the products of a code's borders with the block's largest magnitude are whole
+numbers of at most 16 bits on a common scale, so a quotient that is not on a
+border is at least 2^-16 of itself away from it and its fp32 rounding stays on
+its side: codes have to be equal.  For f32 inputs they have to lie between those
+of the quotient 2^-23 lower and higher.
+
+Product: a matrix instruction adds 128 products, the blocks are added in fp32;
+with each of the K additions and the blocks' scalings off by at most one unit of
+2^-23 of the sum of magnitudes, (K + 16) 2^-23 of that sum bounds the whole; the
+output's rounding adds half a step."""
+
+import numpy as np
+import pytest
+import torch
+
+import implicit_gemm_conv_dp_amd as skg
+from oracle import codecs, projection as pj
+
+pytestmark = pytest.mark.gpu
+
+T = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25, "f32": 2.0 ** -150}   # half a subnormal step
+DIRECT = ["16x16x128", "16x32x128", "32x32x128", "32x64x128", "64x64x128"]
+RING = []
+
+
+def f64(t):
+    return t.cpu().to(torch.float64).numpy()
+
+
+def poison(*shape, dtype=torch.uint8):
+    t = torch.empty(shape, dtype=dtype, device="cuda")
+    t.view(torch.uint8).fill_(0xFF)
+    return t
+
+
+def matrix(seed, rows, cols, dtype, ld=None):
+    """Large and small channels, an empty row and a tiny one, NaN padding."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(torch.randn(cols, generator=g))
+    if rows > 2:
+        x[1] = 0
+        x[2] *= 2.0 ** -12
+    buf = torch.full((rows, ld or cols), float("nan"))
+    buf[:, :cols] = x
+    return buf.to(T[dtype]).cuda()
+
+
+def check_codes(got, x, fmt, block, dtype, label):
+    (s, q), (gs, gq) = pj.block_quantize(x, fmt, block), got
+    assert np.array_equal(gs, s), "%s: %d scales differ" % (label, (gs != s).sum())
+    if dtype != "f32":
+        bad = gq != q
+    else:
+        lo, hi = (codecs.decode(fmt, pj.block_quantize(x, fmt, block, e)[1]) for e in (-2.0 ** -23, 2.0 ** -23))
+        v = codecs.decode(fmt, gq)
+        bad = (v < np.minimum(lo, hi)) | (v > np.maximum(lo, hi)) | (np.signbit(v) != np.signbit(codecs.decode(fmt, q)))
+    assert not bad.any(), "%s: %d codes, first %s" % (label, bad.sum(), np.argwhere(bad)[:3])
+
+
+SHAPES = [(1, 1), (3, 7), (5, 128), (2, 129), (130, 9), (128, 256), (129, 255), (257, 383), (300, 1030)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block", ["1x128", "128x128"])
+def test_quantisation(rows, cols, dtype, fmt, block):
+    x = matrix(rows + cols, rows, cols, dtype, cols + 5)
+    want = f64(x)[:, :cols]
+    kq, kqt = pj.up(cols, 128), pj.up(rows, 128)
+    tall = block == "128x128"
+    for which in ("rows", "columns", "both"):
+        q, qt = poison(rows, kq + 16), poison(cols, kqt + 16)
+        s = poison(kq // 128, -(-rows // 128) if tall else rows, dtype=torch.float32)
+        st = poison(kqt // 128, -(-cols // 128) if tall else cols, dtype=torch.float32)
+        skg.block_quant(x, q if which != "columns" else None, s if which != "columns" else None,
+                        qt if which != "rows" else None, st if which != "rows" else None, rows=rows, cols=cols,
+                        dtype=dtype, dtype_q=fmt, block=block, ldx=cols + 5, ldq=kq + 16, ldqt=kqt + 16)
+        torch.cuda.synchronize()
+        assert (q[:, kq:] == 0xFF).all() and (qt[:, kqt:] == 0xFF).all()
+        if which != "columns":
+            check_codes((s.cpu().numpy(), q[:, :kq].cpu().numpy()), want, fmt, block, dtype, "rows")
+        else:
+            assert (q == 0xFF).all()
+        if which != "rows":
+            check_codes((st.cpu().numpy(), qt[:, :kqt].cpu().numpy()), want.T, fmt, block, dtype, "columns")
+        else:
+            assert (qt == 0xFF).all()
+
+
+@pytest.mark.parametrize("block", ["1x128", "128x128"])
+def test_more_padding_than_needed(block):
+    x = matrix(3, 100, 200, "bf16")
+    tall = block == "128x128"
+    q, qt = poison(100, 384), poison(200, 384)
+    s = poison(3, 1 if tall else 100, dtype=torch.float32)
+    st = poison(3, 2 if tall else 200, dtype=torch.float32)
+    skg.block_quant(x, q, s, qt, st, rows=100, cols=200, dtype="bf16", dtype_q="e4m3", block=block, kq=384, kqt=384)
+    pad = np.zeros((384, 384))
+    pad[:100, :200] = f64(x)
+    for got, w, n in ((q, pad, 100), (qt, pad.T, 200)):
+        sc = s if got is q else st
+        ws, wq = pj.block_quantize(w[:n], "e4m3", block)
+        assert np.array_equal(got.cpu().numpy(), wq) and np.array_equal(sc.cpu().numpy(), ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_extreme_blocks(dtype, fmt):
+    """Subnormals, the largest magnitudes, empty blocks; infinities and NaN stay in
+    their block."""
+    rows = 6
+    x = torch.zeros(rows, 256, dtype=torch.float64)
+    g = torch.Generator().manual_seed(5)
+    x[0] = torch.randn(256, generator=g) * 2.0 ** -130
+    x[1] = torch.randn(256, generator=g).clamp(-1, 1) * 2.0 ** 127.4
+    x[2, 3] = 2.0 ** -126
+    x[3] = torch.randn(256, generator=g) * 2.0 ** -110
+    x[5] = -0.0
+    x = x.to(T[dtype])
+    q, s = poison(rows, 256), poison(2, rows, dtype=torch.float32)
+    kw = dict(rows=rows, cols=256, dtype=dtype, dtype_q=fmt)
+    skg.block_quant(x.cuda(), q, s, **kw)
+    check_codes((s.cpu().numpy(), q.cpu().numpy()), f64(x), fmt, "1x128", dtype, "extreme")
+    y = x.clone()
+    y[2, 100], y[3, 200], y[4, 0] = float("nan"), float("inf"), -float("inf")
+    q2, s2 = poison(rows, 256), poison(2, rows, dtype=torch.float32)
+    skg.block_quant(y.cuda(), q2, s2, **kw)
+    v = codecs.decode(fmt, q2.cpu().numpy()).reshape(rows, 2, 128)
+    bad = np.isnan(s2.cpu().numpy().T)
+    assert np.array_equal(bad, [[0, 0], [0, 0], [1, 0], [0, 1], [1, 0], [0, 0]])
+    assert np.isnan(v[bad]).all()
+    assert np.array_equal(q2.cpu().numpy().reshape(rows, 2, 128)[~bad], q.cpu().numpy().reshape(rows, 2, 128)[~bad])
+
+
+# --- the product ---------------------------------------------------------------
+def operand(seed, rows, K, fmt, block, exact=False):
+    rng = np.random.default_rng(seed)
+    lines = -(-rows // 128) if block == "128x128" else rows
+    if exact:   # sums of few small whole numbers times powers of two: no rounding
+        v = rng.integers(-2, 3, (rows, K)) * (rng.random((rows, K)) < 0.2)
+        q = codecs.encode(fmt, v.astype(np.float64))
+        s = 2.0 ** rng.integers(-2, 3, (K // 128, lines))
+    else:
+        x = rng.standard_normal((rows, K)) * np.exp(0.7 * rng.standard_normal((rows, 1)))
+        s, q = pj.block_quantize(x, fmt, block)
+    s = s.astype(np.float32)
+    return torch.from_numpy(q.astype(np.uint8)).cuda(), torch.from_numpy(s).cuda(), pj.block_values(s, q, fmt, block)
+
+
+def multiply(a, sa, b, sb, C, **kw):
+    skg.gemm(a, b, C, sa, sb, **dict(dict(mode="auto", reduction="auto", ctas=-1), **kw))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tile", DIRECT + RING + ["auto"])
+@pytest.mark.parametrize("scale_mode", ["block128", "row128"])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 128), (17, 40, 384), (65, 132, 1152), (130, 300, 640), (257, 520, 256)])
+def test_product_of_whole_numbers(tile, scale_mode, M, N, K):
+    fmt = "e4m3" if N != 132 else "e5m2"
+    block = "128x128" if scale_mode == "block128" else "1x128"
+    a, sa, A = operand(1, M, K, fmt, "1x128", True)
+    b, sb, B = operand(2, N, K, fmt, block, True)
+    ldc = pj.up(N, 8) + 8
+    C = poison(M, ldc, dtype=torch.float32)
+    multiply(a, sa, b, sb, C, M=M, N=N, K=K, ldc=ldc, dtype_ab=fmt, dtype_c="f32", scale_mode=scale_mode, tile=tile)
+    got = f64(C)
+    assert np.array_equal(got[:, :N], A @ B.T) and np.isnan(got[:, N:]).all()
+
+
+@pytest.mark.parametrize("tile", DIRECT + RING + ["auto"])
+@pytest.mark.parametrize("scale_mode", ["block128", "row128"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype_c", ["bf16", "f16", "f32"])
+def test_product(tile, scale_mode, fmt, dtype_c):
+    M, N, K, ldc = 261, 397, 896, 408
+    block = "128x128" if scale_mode == "block128" else "1x128"
+    a, sa, A = operand(3, M, K, fmt, "1x128")
+    b, sb, B = operand(4, N, K, fmt, block)
+    C = poison(M, ldc, dtype=T[dtype_c])
+    multiply(a, sa, b, sb, C, M=M, N=N, K=K, ldc=ldc, dtype_ab=fmt, dtype_c=dtype_c, scale_mode=scale_mode, tile=tile)
+    got, want = f64(C), A @ B.T
+    tol = (K + 16) * 2.0 ** -23 * (np.abs(A) @ np.abs(B).T)
+    tol += HALF[dtype_c] * (np.abs(want) + tol) + TINY[dtype_c]
+    assert np.all(np.abs(got[:, :N] - want) <= tol) and np.isnan(got[:, N:]).all()
+
+
+@pytest.mark.parametrize("tile", DIRECT + RING)
+def test_operands_in_wider_buffers(tile):
+    """Pitches over K whose padding would be seen, and NaN codes past the end."""
+    M, N, K = 70, 90, 384
+    a, sa, A = operand(5, M, K, "e4m3", "1x128", True)
+    b, sb, B = operand(6, N, K, "e4m3", "1x128", True)
+    wa, wb = poison(M + 2, K + 48), poison(N + 2, K + 16)
+    wa[:M, :K], wb[:N, :K] = a, b
+    C = poison(M, 96, dtype=torch.float32)
+    multiply(wa, sa, wb, sb, C, M=M, N=N, K=K, lda=K + 48, ldb=K + 16, ldc=96, dtype_ab="e4m3", dtype_c="f32",
+             scale_mode="row128", tile=tile)
+    got = f64(C)
+    assert np.array_equal(got[:, :N], A @ B.T) and np.isnan(got[:, N:]).all()
+
+
+@pytest.mark.parametrize("tile", DIRECT + RING)
+def test_nan_stays_in_its_row_and_column(tile):
+    M, N, K = 40, 56, 256
+    a, sa, A = operand(7, M, K, "e4m3", "1x128", True)
+    b, sb, B = operand(8, N, K, "e4m3", "1x128", True)
+    a[3, 200] = 0x7F
+    sb[1, 5] = float("nan")
+    sa[0, 9] = float("inf")
+    C = poison(M, 56, dtype=torch.float32)
+    multiply(a, sa, b, sb, C, M=M, N=N, K=K, dtype_ab="e4m3", dtype_c="f32", scale_mode="row128", tile=tile)
+    got, want = f64(C), A @ B.T
+    bad = np.zeros((M, N), bool)
+    bad[3], bad[:, 5], bad[9] = True, True, True
+    assert np.isnan(got[3]).all() and np.isnan(got[:, 5]).all()
+    assert np.array_equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("scale_mode", ["block128", "row128"])
+def test_captured_product_and_quantiser(scale_mode):
+    M, N, K = 77, 264, 512
+    block = "128x128" if scale_mode == "block128" else "1x128"
+    b, sb, B = operand(9, N, K, "e4m3", block)
+    x = matrix(20, M, K, "bf16")
+    q, s = poison(M, K), poison(K // 128, M, dtype=torch.float32)
+    C = poison(M, N, dtype=torch.bfloat16)
+
+    def step():
+        skg.block_quant(x, q, s, rows=M, cols=K, dtype="bf16", dtype_q="e4m3")
+        skg.gemm(q, b, C, s, sb, M=M, N=N, K=K, dtype_ab="e4m3", dtype_c="bf16", scale_mode=scale_mode,
+                 tile="auto", mode="auto", reduction="auto", ctas=-1)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(4):
+        x.copy_(matrix(21 + i, M, K, "bf16"))
+        step()
+        torch.cuda.synchronize()
+        eager = C.clone()
+        for t in (q, s, C):
+            t.view(torch.uint8).fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C.view(torch.int16), eager.view(torch.int16)), i
+
+
+def test_repeated_launches_give_the_same_bits():
+    M, N, K = 300, 520, 1024
+    a, sa, _ = operand(10, M, K, "e4m3", "1x128")
+    b, sb, _ = operand(11, N, K, "e4m3", "128x128")
+    for tile in DIRECT + RING:
+        first = None
+        for _ in range(4):
+            C = poison(M, N, dtype=torch.float32)
+            multiply(a, sa, b, sb, C, M=M, N=N, K=K, dtype_ab="e4m3", dtype_c="f32", scale_mode="block128", tile=tile)
+            first = C if first is None else first
+            assert torch.equal(C, first)
