@@ -12,11 +12,55 @@
 
 namespace skg {
 
-// Codes of 128 elements of 16 rows of B and of A: element e of lane l is row
-// l % 16 (of A), column 4 (l / 16) + e (of B).
+// The 8-bit matrix instructions do not add their products in full: what lies some
+// 2^-12 under the largest product of a group is dropped (measured, the same for
+// every shape of them; sums of normal data come out 1.3e-5 off).  That is 1/300 of
+// a bf16 result's rounding and 1/18 of an fp16 one's, so 16-bit outputs take them.
+// fp32 outputs (EXACT) take the codes as fp16, which holds them all, through the
+// fp16 instructions at half the rate: 8e-9 off.
+
+// Codes of 128 elements of a row, 32 a lane, as an instruction takes them.
+template <int FMT, bool EXACT>
+struct F8Frag;
 template <int FMT>
-SKG_DEV f32x4 f8_block(const i32x8& b, const i32x8& a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.f, 0.f, 0.f, 0.f}, FMT, FMT, 0, 0, 0, 0);
+struct F8Frag<FMT, false> {
+  i32x8 v;
+  SKG_DEV void set(const i32x8& codes) { v = codes; }
+};
+template <int FMT>
+struct F8Frag<FMT, true> {
+  f16x8 v[4];
+  SKG_DEV void set(const i32x8& codes) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f16x2 lo, hi;
+      if constexpr (FMT == 0) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.f, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.f, true);
+      } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes[i], 1.f, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes[i], 1.f, true);
+      }
+      v[i / 2][i % 2 * 4] = lo[0];
+      v[i / 2][i % 2 * 4 + 1] = lo[1];
+      v[i / 2][i % 2 * 4 + 2] = hi[0];
+      v[i / 2][i % 2 * 4 + 3] = hi[1];
+    }
+  }
+};
+// Their products' sums over the block: element e of lane l is row l % 16 (of A),
+// column 4 (l / 16) + e (of B).
+template <int FMT>
+SKG_DEV f32x4 f8_block(const F8Frag<FMT, false>& b, const F8Frag<FMT, false>& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, FMT, FMT, 0, 0, 0, 0);
+}
+template <int FMT>
+SKG_DEV f32x4 f8_block(const F8Frag<FMT, true>& b, const F8Frag<FMT, true>& a) {
+  f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 4; ++h) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[h], a.v[h], t, 0, 0, 0);
+  return t;
 }
 SKG_DEV i32x8 f8_frag(const SKG_LDS char* rows, int row, int lane) {
   const i32x4 lo = *(const SKG_LDS i32x4*)(rows + lds_off<128>(row, 2 * (lane >> 4)));
@@ -34,7 +78,7 @@ SKG_DEV i32x4 f8_scales(const float* s, int64_t lines, int64_t width) {
 // The four waves of a workgroup split K; each streams its own blocks, without a
 // barrier, through LDS of its own, D blocks ahead.  The four partial tiles meet
 // once in LDS and are added in a fixed order: one launch, no workspace.
-template <int FM, int FN, int D, int FMT, bool ROWS>
+template <int FM, int FN, int D, int FMT, bool ROWS, bool EXACT>
 struct F8Direct {
   static constexpr int TM = 16 * FM, TN = 16 * FN, WAVES = 4, RB = 128;
   static constexpr int UA = TM / 8, UB = TN / 8, PER = UA + UB + 2;
@@ -93,17 +137,17 @@ struct F8Direct {
     const SKG_LDS char* st = lds + at * SLOT;
     const int r = lane & 15, q = lane >> 4;
     const SKG_LDS float* sc = (const SKG_LDS float*)(st + XOFF);
-    i32x8 a[FM], b[FN];
+    F8Frag<FMT, EXACT> a[FM], b[FN];
     float sa[FM];
     f32x4 sb[FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
-      a[f] = f8_frag(st, f * 16 + r, lane);
+      a[f].set(f8_frag(st, f * 16 + r, lane));
       sa[f] = sc[f * 16 + r];
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
-      b[f] = f8_frag(st + TM * RB, f * 16 + r, lane);
+      b[f].set(f8_frag(st + TM * RB, f * 16 + r, lane));
       sb[f] = *(const SKG_LDS f32x4*)(sc + 64 + f * 16 + 4 * q);
     }
 #pragma unroll
@@ -179,7 +223,7 @@ struct F8Direct {
       const int m = m0 + f / FN * 16 + (lane & 15), n = n0 + f % FN * 16 + 4 * (lane >> 4);
       if (m >= g.M || n >= g.N) continue;
       const size_t o = (size_t)m * g.ldc + n;
-      if (g.dtype_c == DT_F32) {
+      if constexpr (EXACT) {
         float* c = (float*)g.C + o;
         if (n + 4 <= g.N) {
           *(f32x4*)c = v;
@@ -201,6 +245,268 @@ struct F8Direct {
   }
 };
 
+// --- many tiles ------------------------------------------------------------------
+// Eight waves on a ring of two stages, a stage a block of 128 of K; wave tile
+// TM/2 x TN/4 in 16 x 16 pieces.  Per stage a wave holds its columns' fragments and
+// two of its rows', reads the next rows' while one's products run, and scales a
+// piece's results two instructions after they were started.
+//
+// At the last row of a stage everything of it has been read: the barrier there
+// frees its slot, which the stage after next is loaded into, and the next stage's
+// fragments are read over the ones that the last row has done with.
+template <int TM_, int TN_, int FMT, bool ROWS, bool EXACT>
+struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
+  typedef Ring8<TM_, TN_, (TM_ + TN_) * 4> R;
+  using R::dst, R::I, R::lane, R::lds, R::na, R::nb, R::ra, R::rb, R::slot, R::wave, R::wm, R::wn, R::XOFF;
+  static constexpr int TM = TM_, TN = TN_, WTM = R::WTM, WTN = R::WTN, RB = 128;
+  static constexpr int FM = WTM / 16, FN = WTN / 16, NP = FM * FN, LAST = (FM - 1) * FN;
+  static constexpr int ROWDMA = R::UA + R::UB, PER = ROWDMA + 1;
+  static constexpr int CA = TM / 64, CB = TN / 64;  // scale DMAs of a stage
+  static_assert(CA + CB <= 8 && FM % 2 == 0 && NP >= 4, "tile");
+  typedef F8Frag<FMT, EXACT> Frag;
+
+  const GemmParams& g;
+  i32x4 rsa, rsb;
+  int nsa, nsb;
+  uint32_t spa, spb, soff;  // pitches of the scales' lines; this lane's place in one
+  uint32_t fra, frb, fsa, fsb;
+  f32x4 acc[FM][FN];
+
+  SKG_DEV F8Ring(const GemmParams& g_, SKG_LDS char* l) : g(g_) {
+    R::init(l, g.lda_b, g.ldb_b, g.K / 128);
+    const int64_t nbk = ROWS ? g.N : (g.N + 127) / 128;
+    rsa = f8_scales(g.sa, I, g.M);
+    rsb = f8_scales(g.sb, I, nbk);
+    nsa = rsa[2];
+    nsb = rsb[2];
+    spa = (uint32_t)g.M * 4;
+    spb = (uint32_t)nbk * 4;
+    const int r = lane & 15, q = lane >> 4;
+    // Rows f * 16 + r: both terms of the row permutation depend on r alone.
+    fra = lds_off<RB>(wm * WTM + r, 2 * q);
+    frb = TM * RB + lds_off<RB>(wn * WTN + r, 2 * q);
+    fsa = XOFF + (wm * WTM + r * FM) * 4;
+    fsb = XOFF + (TM + wn * WTN + 4 * q) * 4;
+  }
+  SKG_DEV void open(int m0, int n0) {
+    ra = ring_rows(g.A, m0, g.M, g.lda_b, (uint32_t)g.K, na);
+    rb = ring_rows(g.B, n0, g.N, g.ldb_b, (uint32_t)g.K, nb);
+    // Scales of A lie in LDS by wave row, lane row and then piece, so that a lane
+    // reads its FM together.
+    if (wave % (CA + CB) < CA) {
+      const int p = wave % (CA + CB) * 64 + lane, in = p % WTM, row = m0 + p / WTM * WTM + in % FM * 16 + in / FM;
+      soff = row < g.M ? (uint32_t)row * 4 : kOOB;
+    } else {
+      const int col = n0 + (wave % (CA + CB) - CA) * 64 + lane;
+      soff = col < g.N ? (uint32_t)(ROWS ? col : col / 128) * 4 : kOOB;
+    }
+  }
+  // DMA N (0 .. PER-1) of stage j: rows, then the wave's share of the scales (waves
+  // beyond the shares repeat one).
+  template <int N>
+  SKG_DEV void dma(int j) const {
+    if constexpr (N < ROWDMA) {
+      R::template dma_rows<N>(j);
+    } else {
+      const bool live = j < I;
+      const int c = wave % (CA + CB);
+      i32x4 r = c < CA ? rsa : rsb;
+      r[2] = live ? (c < CA ? nsa : nsb) : 0;
+      ring_dma4(r, dst(j) + XOFF + c * 256, soff, live ? (uint32_t)j * (c < CA ? spa : spb) : 0);
+    }
+  }
+  SKG_DEV i32x8 read(uint32_t at) const {
+    // The two 16-byte chunks of a lane are neighbours: 2q and 2q + 1 differ in the
+    // lowest bit of the permuted chunk.
+    const i32x4 lo = *(const SKG_LDS i32x4*)(lds + at), hi = *(const SKG_LDS i32x4*)(lds + (at ^ 16));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  SKG_DEV i32x8 read_a(uint32_t st, int f) const { return read(st + fra + f * 16 * RB); }
+  SKG_DEV i32x8 read_b(uint32_t st, int n) const { return read(st + frb + n * 16 * RB); }
+  struct Scales {
+    float a[FM];
+    f32x4 b[ROWS ? FN : 1];
+  };
+  SKG_DEV void read_scales(Scales& s, uint32_t st) const {
+#pragma unroll
+    for (int f = 0; f < FM; f += 4) {
+      const f32x4 v = *(const SKG_LDS f32x4*)(lds + st + fsa + f * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.a[f + e] = v[e];
+    }
+    if constexpr (ROWS) {
+#pragma unroll
+      for (int n = 0; n < FN; ++n) s.b[n] = *(const SKG_LDS f32x4*)(lds + st + fsb + n * 64);
+    } else {
+      s.b[0][0] = *(const SKG_LDS float*)(lds + st + fsb);  // one for all of a wave's columns
+    }
+  }
+  template <int P>
+  SKG_DEV void scale(const f32x4 (&t)[3], const Scales& s) {
+    constexpr int f = P / FN, n = P % FN;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[f][n][e] = __builtin_fmaf(t[P % 3][e], ROWS ? s.a[f] * s.b[n][e] : s.a[f], acc[f][n][e]);
+  }
+
+  SKG_DEV void iteration(Frag (&a)[2], Frag (&b)[FN], Scales& s, int i) {
+    const uint32_t cur = slot(i), nxt = slot(i + 1);
+    f32x4 t[3];
+    if constexpr (!ROWS) {
+#pragma unroll
+      for (int f = 0; f < FM; ++f) s.a[f] *= s.b[0][0];
+    }
+    i32x8 raw;
+    static_for<0, LAST>([&](auto p_) {
+      constexpr int p = decltype(p_)::value, f = p / FN, n = p % FN;
+      t[p % 3] = f8_block<FMT>(b[n], a[f & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (n == 0) raw = read_a(cur, f + 1);
+      if constexpr (n == FN - 1) a[(f + 1) & 1].set(raw);
+      if constexpr (p >= 2) scale<p - 2>(t, s);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_vm<0>();  // stage i + 1
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    i32x8 rb_[EXACT ? FN : 1];
+    static_for<LAST, NP>([&](auto p_) {
+      constexpr int p = decltype(p_)::value, n = p % FN;
+      t[p % 3] = f8_block<FMT>(b[n], a[(FM - 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (n == 0) raw = read_a(nxt, 0);
+      if constexpr (EXACT)
+        rb_[n] = read_b(nxt, n);
+      else
+        b[n].set(read_b(nxt, n));
+      static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + 2); });
+      scale<p - 2>(t, s);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    scale<NP - 2>(t, s);
+    scale<NP - 1>(t, s);
+    a[0].set(raw);
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int n = 0; n < FN; ++n) b[n].set(rb_[n]);
+    }
+    read_scales(s, nxt);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  SKG_DEV void ahead() {
+    static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(0); });
+  }
+  // Stage 0 is on its way.
+  SKG_DEV void mainloop() {
+    static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(1); });
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    wait_vm<PER>();
+    lds_barrier();
+    Frag a[2], b[FN];
+    Scales s;
+    a[0].set(read_a(slot(0), 0));
+#pragma unroll
+    for (int n = 0; n < FN; ++n) b[n].set(read_b(slot(0), n));
+    read_scales(s, slot(0));
+#pragma unroll 1
+    for (int i = 0; i < I; ++i) iteration(a, b, s, i);
+    wait_vm<0>();  // the refills past the end
+    lds_barrier();
+  }
+
+  // The wave's part of the tile, 16 rows at a time through LDS of its own, so that
+  // memory sees whole rows.
+  template <int DTC>
+  SKG_DEV void store_tile(int m0, int n0, SKG_LDS char* strips) const {
+    constexpr int ES = DTC == DT_F32 ? 4 : 2;
+    static_assert(8 * 16 * WTN * ES <= R::SLOT, "strips fit the slot");
+    SKG_LDS char* st = strips + wave * 16 * WTN * ES;
+    const int r = lane & 15, q = lane >> 4;
+    static_for<0, FM>([&](auto f_) {
+      constexpr int f = decltype(f_)::value;
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        const f32x4 v = acc[f][n];
+        if constexpr (DTC == DT_F32)
+          *(SKG_LDS f32x4*)(st + strip_off<4, WTN>(r, n * 4 + q)) = v;
+        else
+          *(SKG_LDS i32x2*)(st + strip_off<2, WTN>(r, n * 2 + (q >> 1)) + (q & 1) * 8) =
+              DTC == DT_F16 ? i32x2{(int)pack_f16x2(v[0], v[1]), (int)pack_f16x2(v[2], v[3])}
+                            : i32x2{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      store_strip<ES, WTN, 16>(st, g.C, g.ldc, m0 + wm * WTM + f * 16, n0 + wn * WTN, g.M, g.N, true);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    });
+  }
+};
+
+template <class T, bool EXACT>
+__global__ __launch_bounds__(512, 1) void f8_ring_kernel(GemmParams g, KPlan p) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
+  T t(g, (SKG_LDS char*)lds);
+  TileRun run(p.tiles_m * p.tiles_n);
+  constexpr int GROUP = 4;  // tile rows of a strip that is walked column by column
+  auto origin = [&](int k, int& m0, int& n0) {
+    const int id = run.first + k, strip = id / (GROUP * p.tiles_n), in = id - strip * GROUP * p.tiles_n;
+    const int rows = min(GROUP, p.tiles_m - strip * GROUP), tn = in / rows;
+    m0 = (strip * GROUP + in - tn * rows) * T::TM;
+    n0 = tn * T::TN;
+    t.open(m0, n0);
+  };
+  int k = run.k, m0, n0;
+  if (k >= run.count) return;
+  origin(k, m0, n0);
+  t.ahead();
+  for (;;) {
+    t.mainloop();
+    // The next tile's first stage travels during this one's copy-out.
+    const int m = m0, n = n0;
+    k += run.per;
+    SKG_LDS char* last = (SKG_LDS char*)lds + t.slot(t.I - 1);
+    if (k < run.count) {
+      origin(k, m0, n0);
+      t.sbase += t.I;
+      t.ahead();
+    }
+    if constexpr (EXACT)
+      t.template store_tile<DT_F32>(m, n, last);
+    else if (g.dtype_c == DT_F16)
+      t.template store_tile<DT_F16>(m, n, last);
+    else
+      t.template store_tile<DT_BF16>(m, n, last);
+    if (k >= run.count) return;
+    lds_barrier();  // every wave is done with the slot the strips went through
+  }
+}
+
+// Both of a tile's kernels: fp32 outputs take the exact one.
+template <class K>
+hipError_t f8_launch(K&& kernel, const KPlan& p, int grid, int threads, const GemmParams& g, hipStream_t st, hipEvent_t ev0,
+                     hipEvent_t ev1) {
+  hipError_t e;
+  if (ev0 && (e = hipEventRecord(ev0, st)) != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, st, g, p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return ev1 ? hipEventRecord(ev1, st) : hipSuccess;
+}
+template <int TM, int TN, int FMT, bool ROWS>
+GemmInst f8_ring() {
+  typedef F8Ring<TM, TN, FMT, ROWS, false> T;
+  typedef F8Ring<TM, TN, FMT, ROWS, true> E;
+  return {[](const GemmParams& g, const KPlan& p, const Scratch&, hipStream_t st, hipEvent_t ev0, hipEvent_t ev1) {
+            const int total = p.tiles_m * p.tiles_n, grid = total < p.cus ? total : p.cus;
+            return g.dtype_c == DT_F32 ? f8_launch(f8_ring_kernel<E, true>, p, grid, 512, g, st, ev0, ev1)
+                                       : f8_launch(f8_ring_kernel<T, false>, p, grid, 512, g, st, ev0, ev1);
+          },
+          [](int* out) { return hipOccupancyMaxActiveBlocksPerMultiprocessor(out, f8_ring_kernel<T, false>, 512, 0); }};
+}
+
 template <class T>
 __global__ __launch_bounds__(256) void f8_direct_kernel(GemmParams g, KPlan p) {
   __shared__ __attribute__((aligned(128))) char lds[T::LDS];
@@ -208,14 +514,13 @@ __global__ __launch_bounds__(256) void f8_direct_kernel(GemmParams g, KPlan p) {
   d.run(g, p, (SKG_LDS char*)lds);
 }
 
-template <class T>
+template <int FM, int FN, int D, int FMT, bool ROWS>
 GemmInst f8_direct() {
+  typedef F8Direct<FM, FN, D, FMT, ROWS, false> T;
+  typedef F8Direct<FM, FN, D, FMT, ROWS, true> E;
   return {[](const GemmParams& g, const KPlan& p, const Scratch&, hipStream_t st, hipEvent_t ev0, hipEvent_t ev1) {
-            hipError_t e;
-            if (ev0 && (e = hipEventRecord(ev0, st)) != hipSuccess) return e;
-            hipLaunchKernelGGL((f8_direct_kernel<T>), dim3(p.grid), dim3(256), 0, st, g, p);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            return ev1 ? hipEventRecord(ev1, st) : hipSuccess;
+            return g.dtype_c == DT_F32 ? f8_launch(f8_direct_kernel<E>, p, p.grid, 256, g, st, ev0, ev1)
+                                       : f8_launch(f8_direct_kernel<T>, p, p.grid, 256, g, st, ev0, ev1);
           },
           [](int* out) { return hipOccupancyMaxActiveBlocksPerMultiprocessor(out, f8_direct_kernel<T>, 256, 0); }};
 }

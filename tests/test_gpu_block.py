@@ -27,7 +27,7 @@ T = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
 TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25, "f32": 2.0 ** -150}   # half a subnormal step
 DIRECT = ["16x16x128", "16x32x128", "32x32x128", "32x64x128", "64x64x128"]
-RING = []
+RING = ["128x128x128", "256x128x128", "256x256x128"]
 
 
 def f64(t):
