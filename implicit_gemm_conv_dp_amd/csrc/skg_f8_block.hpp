@@ -246,18 +246,19 @@ struct F8Direct {
 };
 
 // --- many tiles ------------------------------------------------------------------
-// Eight waves on a ring of two stages, a stage a block of 128 of K; wave tile
+// Eight waves on a ring of D stages, a stage a block of 128 of K; wave tile
 // TM/2 x TN/4 in 16 x 16 pieces.  Per stage a wave holds its columns' fragments and
 // two of its rows', reads the next rows' while one's products run, and scales a
 // piece's results two instructions after they were started.
 //
 // At the last row of a stage everything of it has been read: the barrier there
-// frees its slot, which the stage after next is loaded into, and the next stage's
-// fragments are read over the ones that the last row has done with.
-template <int TM_, int TN_, int FMT, bool ROWS, bool EXACT>
-struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
-  typedef Ring8<TM_, TN_, (TM_ + TN_) * 4> R;
-  using R::dst, R::I, R::lane, R::lds, R::na, R::nb, R::ra, R::rb, R::slot, R::wave, R::wm, R::wn, R::XOFF;
+// frees its slot, which stage i + D is loaded into, and the next stage's fragments
+// are read over the ones that the last row has done with.
+template <int TM_, int TN_, int D_, int FMT, bool ROWS, bool EXACT>
+struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
+  typedef Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> R;
+  static constexpr int D = D_;
+  using R::dst, R::step, R::I, R::lane, R::lds, R::na, R::nb, R::ra, R::rb, R::slot, R::wave, R::wm, R::wn, R::XOFF;
   static constexpr int TM = TM_, TN = TN_, WTM = R::WTM, WTN = R::WTN, RB = 128;
   static constexpr int FM = WTM / 16, FN = WTN / 16, NP = FM * FN, LAST = (FM - 1) * FN;
   static constexpr int ROWDMA = R::UA + R::UB, PER = ROWDMA + 1;
@@ -301,18 +302,18 @@ struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
       soff = col < g.N ? (uint32_t)(ROWS ? col : col / 128) * 4 : kOOB;
     }
   }
-  // DMA N (0 .. PER-1) of stage j: rows, then the wave's share of the scales (waves
-  // beyond the shares repeat one).
+  // DMA N (0 .. PER-1) of stage j into the slot at `to`: rows, then the wave's share
+  // of the scales (waves beyond the shares repeat one).
   template <int N>
-  SKG_DEV void dma(int j) const {
+  SKG_DEV void dma(int j, uint32_t to) const {
     if constexpr (N < ROWDMA) {
-      R::template dma_rows<N>(j);
+      R::template dma_rows<N>(j, to);
     } else {
       const bool live = j < I;
       const int c = wave % (CA + CB);
       i32x4 r = c < CA ? rsa : rsb;
       r[2] = live ? (c < CA ? nsa : nsb) : 0;
-      ring_dma4(r, dst(j) + XOFF + c * 256, soff, live ? (uint32_t)j * (c < CA ? spa : spb) : 0);
+      ring_dma4(r, to + XOFF + c * 256, soff, live ? (uint32_t)j * (c < CA ? spa : spb) : 0);
     }
   }
   SKG_DEV i32x8 read(uint32_t at) const {
@@ -350,7 +351,7 @@ struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
   }
 
   SKG_DEV void iteration(Frag (&a)[2], Frag (&b)[FN], Scales& s, int i) {
-    const uint32_t cur = slot(i), nxt = slot(i + 1);
+    const uint32_t cur = slot(0), nxt = slot(1), to = dst(0);
     f32x4 t[3];
     if constexpr (!ROWS) {
 #pragma unroll
@@ -367,7 +368,7 @@ struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
       __builtin_amdgcn_sched_barrier(0);
     });
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_vm<0>();  // stage i + 1
+    wait_vm<(D - 2) * PER>();  // stage i + 1 has landed: the younger ones have not
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     i32x8 rb_[EXACT ? FN : 1];
@@ -380,7 +381,7 @@ struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
         rb_[n] = read_b(nxt, n);
       else
         b[n].set(read_b(nxt, n));
-      static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + 2); });
+      static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + D, to); });
       scale<p - 2>(t, s);
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -393,19 +394,23 @@ struct F8Ring : Ring8<TM_, TN_, (TM_ + TN_) * 4> {
     }
     read_scales(s, nxt);
     __builtin_amdgcn_sched_barrier(0);
+    step();
   }
 
+  // All stages of the ring but the last, whose slot the copy-out takes.
   SKG_DEV void ahead() {
-    static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(0); });
+    static_for<0, D - 1>([&](auto j_) {
+      constexpr int j = decltype(j_)::value;
+      static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(j, dst(j)); });
+    });
   }
-  // Stage 0 is on its way.
   SKG_DEV void mainloop() {
-    static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(1); });
+    static_for<0, PER>([&](auto n_) { dma<decltype(n_)::value>(D - 1, dst(D - 1)); });
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
       for (int n = 0; n < FN; ++n) acc[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    wait_vm<PER>();
+    wait_vm<(D - 1) * PER>();
     lds_barrier();
     Frag a[2], b[FN];
     Scales s;
@@ -468,10 +473,9 @@ __global__ __launch_bounds__(512, 1) void f8_ring_kernel(GemmParams g, KPlan p) 
     // The next tile's first stage travels during this one's copy-out.
     const int m = m0, n = n0;
     k += run.per;
-    SKG_LDS char* last = (SKG_LDS char*)lds + t.slot(t.I - 1);
+    SKG_LDS char* last = (SKG_LDS char*)lds + t.slot(T::D - 1);  // the stage that ran last
     if (k < run.count) {
       origin(k, m0, n0);
-      t.sbase += t.I;
       t.ahead();
     }
     if constexpr (EXACT)
@@ -495,10 +499,10 @@ hipError_t f8_launch(K&& kernel, const KPlan& p, int grid, int threads, const Ge
   if ((e = hipGetLastError()) != hipSuccess) return e;
   return ev1 ? hipEventRecord(ev1, st) : hipSuccess;
 }
-template <int TM, int TN, int FMT, bool ROWS>
+template <int TM, int TN, int D, int FMT, bool ROWS>
 GemmInst f8_ring() {
-  typedef F8Ring<TM, TN, FMT, ROWS, false> T;
-  typedef F8Ring<TM, TN, FMT, ROWS, true> E;
+  typedef F8Ring<TM, TN, D, FMT, ROWS, false> T;
+  typedef F8Ring<TM, TN, D, FMT, ROWS, true> E;
   return {[](const GemmParams& g, const KPlan& p, const Scratch&, hipStream_t st, hipEvent_t ev0, hipEvent_t ev1) {
             const int total = p.tiles_m * p.tiles_n, grid = total < p.cus ? total : p.cus;
             return g.dtype_c == DT_F32 ? f8_launch(f8_ring_kernel<E, true>, p, grid, 512, g, st, ev0, ev1)

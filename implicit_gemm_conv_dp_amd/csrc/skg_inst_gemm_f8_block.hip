@@ -13,9 +13,9 @@ GemmInst block_by_tile(int tile_id) {
     case SKG_TILE_32x32x128: return f8_direct<2, 2, 2, FMT, ROWS>();
     case SKG_TILE_32x64x128: return f8_direct<2, 4, 3, FMT, ROWS>();
     case SKG_TILE_64x64x128: return f8_direct<4, 4, 2, FMT, ROWS>();
-    case SKG_TILE_128x128x128: return f8_ring<128, 128, FMT, ROWS>();
-    case SKG_TILE_256x128x128: return f8_ring<256, 128, FMT, ROWS>();
-    case SKG_TILE_256x256x128: return f8_ring<256, 256, FMT, ROWS>();
+    case SKG_TILE_128x128x128: return f8_ring<128, 128, 4, FMT, ROWS>();
+    case SKG_TILE_256x128x128: return f8_ring<256, 128, 3, FMT, ROWS>();
+    case SKG_TILE_256x256x128: return f8_ring<256, 256, 2, FMT, ROWS>();
     default: return {nullptr, nullptr};
   }
 }

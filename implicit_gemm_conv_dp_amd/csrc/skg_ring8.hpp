@@ -1,5 +1,5 @@
 // Frame of the products that eight waves (2 x 4) of a workgroup compute on a ring
-// of two direct-to-LDS stages: the stages' loads and the copy-out.
+// of direct-to-LDS stages: the stages' loads and the copy-out.
 //
 // A stage is 128 bytes of K of the tile's TM rows of A, then of its TN rows of B,
 // then EXTRA bytes that the product adds.  Two waves a SIMD: one issues vector
@@ -76,19 +76,19 @@ SKG_DEV void store_strip(const SKG_LDS char* st, char* C, int64_t ldc, int m0, i
   }
 }
 
-template <int TM_, int TN_, int EXTRA_>
+template <int TM_, int TN_, int D_, int EXTRA_>
 struct Ring8 {
-  static constexpr int TM = TM_, TN = TN_, RB = 128, THREADS = 512;
+  static constexpr int TM = TM_, TN = TN_, D = D_, RB = 128, THREADS = 512;
   static constexpr int WTM = TM / 2, WTN = TN / 4;
   static constexpr int UA = TM / 64, UB = TN / 64;  // row DMAs a wave and stage
   static constexpr int EXTRA = EXTRA_, SLOT = (TM + TN) * RB + EXTRA;
-  static constexpr int LDS = 2 * SLOT;
+  static constexpr int LDS = D * SLOT;
   static constexpr int XOFF = (TM + TN) * RB;
   static_assert(LDS <= 160 * 1024, "LDS");
 
   SKG_LDS char* lds;
   int lane, wave, wm, wn, I;  // I: stages of a tile
-  uint32_t sbase;             // ring entry of the tile's stage 0
+  int at;                     // ring entry of the stage that runs
   uint32_t offa[UA], offb[UB];
   i32x4 ra, rb;
   int na, nb;
@@ -100,7 +100,7 @@ struct Ring8 {
     wm = wave >> 2;
     wn = wave & 3;
     I = stages;
-    sbase = 0;
+    at = 0;
     int row, chunk;
     lds_slot<RB>(threadIdx.x, row, chunk);
 #pragma unroll
@@ -108,21 +108,27 @@ struct Ring8 {
 #pragma unroll
     for (int u = 0; u < UB; ++u) offb[u] = (uint32_t)(row + 64 * u) * ldb_b + chunk * 16;
   }
-  SKG_DEV uint32_t slot(int j) const { return ((sbase + j) & 1) * SLOT; }
-  SKG_DEV uint32_t dst(int j) const { return lds_addr(lds) + slot(j); }
-  // Row DMA N (0 .. UA+UB-1) of stage j; a stage past the end reads nothing.
+  // Offset of the slot of the stage `ahead` (0 .. D) after the one that runs.
+  SKG_DEV uint32_t slot(int ahead) const {
+    const int s = at + ahead;
+    return (s >= D ? s - D : s) * SLOT;
+  }
+  SKG_DEV void step() { at = at + 1 == D ? 0 : at + 1; }
+  SKG_DEV uint32_t dst(int ahead) const { return lds_addr(lds) + slot(ahead); }
+  // Row DMA N (0 .. UA+UB-1) of stage j into the slot at LDS address `to`; a stage
+  // past the end reads nothing.
   template <int N>
-  SKG_DEV void dma_rows(int j) const {
+  SKG_DEV void dma_rows(int j, uint32_t to) const {
     const bool live = j < I;
     const uint32_t kb = live ? (uint32_t)j * RB : 0;
     if constexpr (N < UB) {
       i32x4 r = rb;
       r[2] = live ? nb : 0;
-      ring_dma16<TM * RB + N * 8192>(r, dst(j) + wave * 1024, offb[N], kb);
+      ring_dma16<TM * RB + N * 8192>(r, to + wave * 1024, offb[N], kb);
     } else {
       i32x4 r = ra;
       r[2] = live ? na : 0;
-      ring_dma16<(N - UB) * 8192>(r, dst(j) + wave * 1024, offa[N - UB], kb);
+      ring_dma16<(N - UB) * 8192>(r, to + wave * 1024, offa[N - UB], kb);
     }
   }
 };
