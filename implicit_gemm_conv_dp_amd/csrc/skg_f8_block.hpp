@@ -263,7 +263,7 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
   static constexpr int FM = WTM / 16, FN = WTN / 16, NP = FM * FN, LAST = (FM - 1) * FN;
   static constexpr int ROWDMA = R::UA + R::UB, PER = ROWDMA + 1;
   static constexpr int CA = TM / 64, CB = TN / 64;  // scale DMAs of a stage
-  static_assert(CA + CB <= 8 && FM % 2 == 0 && NP >= 4, "tile");
+  static_assert(CA + CB <= 8 && FM % 2 == 0 && NP % 4 == 0 && LAST >= 2, "tile");
   typedef F8Frag<FMT, EXACT> Frag;
 
   const GemmParams& g;
@@ -316,14 +316,18 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
       ring_dma4(r, to + XOFF + c * 256, soff, live ? (uint32_t)j * (c < CA ? spa : spb) : 0);
     }
   }
-  SKG_DEV i32x8 read(uint32_t at) const {
-    // The two 16-byte chunks of a lane are neighbours: 2q and 2q + 1 differ in the
-    // lowest bit of the permuted chunk.
-    const i32x4 lo = *(const SKG_LDS i32x4*)(lds + at), hi = *(const SKG_LDS i32x4*)(lds + (at ^ 16));
+  // A lane's two 16-byte chunks of a row are neighbours: 2q and 2q + 1 differ in the
+  // lowest bit of the permuted chunk.  Their addresses within a slot are kept, and
+  // the pieces' rows are the reads' constant offsets.
+  struct At {
+    const SKG_LDS char *lo, *hi;
+  };
+  SKG_DEV At rows_at(uint32_t st, uint32_t first) const { return {lds + (st + first), lds + ((st + first) ^ 16)}; }
+  template <int F>
+  SKG_DEV static i32x8 read(const At& p) {
+    const i32x4 lo = *(const SKG_LDS i32x4*)(p.lo + F * 16 * RB), hi = *(const SKG_LDS i32x4*)(p.hi + F * 16 * RB);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
-  SKG_DEV i32x8 read_a(uint32_t st, int f) const { return read(st + fra + f * 16 * RB); }
-  SKG_DEV i32x8 read_b(uint32_t st, int n) const { return read(st + frb + n * 16 * RB); }
   struct Scales {
     float a[FM];
     f32x4 b[ROWS ? FN : 1];
@@ -343,56 +347,60 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
     }
   }
   template <int P>
-  SKG_DEV void scale(const f32x4 (&t)[3], const Scales& s) {
+  SKG_DEV void scale(const f32x4 (&t)[4], const Scales& s) {
     constexpr int f = P / FN, n = P % FN;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      acc[f][n][e] = __builtin_fmaf(t[P % 3][e], ROWS ? s.a[f] * s.b[n][e] : s.a[f], acc[f][n][e]);
+      acc[f][n][e] = __builtin_fmaf(t[P % 4][e], ROWS ? s.a[f] * s.b[n][e] : s.a[f], acc[f][n][e]);
   }
 
-  SKG_DEV void iteration(Frag (&a)[2], Frag (&b)[FN], Scales& s, int i) {
+  // The last two results of an iteration are scaled in the next one's first steps,
+  // while its products run.
+  SKG_DEV void iteration(Frag (&a)[2], Frag (&b)[FN], f32x4 (&t)[4], Scales& s, int i) {
     const uint32_t cur = slot(0), nxt = slot(1), to = dst(0);
-    f32x4 t[3];
-    if constexpr (!ROWS) {
-#pragma unroll
-      for (int f = 0; f < FM; ++f) s.a[f] *= s.b[0][0];
-    }
+    const At ca = rows_at(cur, fra);
     i32x8 raw;
     static_for<0, LAST>([&](auto p_) {
       constexpr int p = decltype(p_)::value, f = p / FN, n = p % FN;
-      t[p % 3] = f8_block<FMT>(b[n], a[f & 1]);
+      t[p % 4] = f8_block<FMT>(b[n], a[f & 1]);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (n == 0) raw = read_a(cur, f + 1);
+      if constexpr (n == 0) raw = read<f + 1>(ca);
       if constexpr (n == FN - 1) a[(f + 1) & 1].set(raw);
-      if constexpr (p >= 2) scale<p - 2>(t, s);
+      if constexpr (p == 2 && !ROWS) {
+#pragma unroll
+        for (int f_ = 0; f_ < FM; ++f_) s.a[f_] *= s.b[0][0];
+      }
+      if constexpr (p >= 2)
+        scale<p - 2>(t, s);
+      else
+        scale<NP - 2 + p>(t, s);
+      if constexpr (p == 1) read_scales(s, cur);
       __builtin_amdgcn_sched_barrier(0);
     });
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wait_vm<(D - 2) * PER>();  // stage i + 1 has landed: the younger ones have not
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    const At na_ = rows_at(nxt, fra), nb_ = rows_at(nxt, frb);
     i32x8 rb_[EXACT ? FN : 1];
     static_for<LAST, NP>([&](auto p_) {
       constexpr int p = decltype(p_)::value, n = p % FN;
-      t[p % 3] = f8_block<FMT>(b[n], a[(FM - 1) & 1]);
+      t[p % 4] = f8_block<FMT>(b[n], a[(FM - 1) & 1]);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (n == 0) raw = read_a(nxt, 0);
+      if constexpr (n == 0) raw = read<0>(na_);
       if constexpr (EXACT)
-        rb_[n] = read_b(nxt, n);
+        rb_[n] = read<n>(nb_);
       else
-        b[n].set(read_b(nxt, n));
+        b[n].set(read<n>(nb_));
       static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + D, to); });
       scale<p - 2>(t, s);
       __builtin_amdgcn_sched_barrier(0);
     });
-    scale<NP - 2>(t, s);
-    scale<NP - 1>(t, s);
     a[0].set(raw);
     if constexpr (EXACT) {
 #pragma unroll
       for (int n = 0; n < FN; ++n) b[n].set(rb_[n]);
     }
-    read_scales(s, nxt);
     __builtin_amdgcn_sched_barrier(0);
     step();
   }
@@ -413,13 +421,15 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
     wait_vm<(D - 1) * PER>();
     lds_barrier();
     Frag a[2], b[FN];
-    Scales s;
-    a[0].set(read_a(slot(0), 0));
-#pragma unroll
-    for (int n = 0; n < FN; ++n) b[n].set(read_b(slot(0), n));
-    read_scales(s, slot(0));
+    a[0].set(read<0>(rows_at(slot(0), fra)));
+    const At bt = rows_at(slot(0), frb);
+    static_for<0, FN>([&](auto n_) { b[decltype(n_)::value].set(read<decltype(n_)::value>(bt)); });
+    Scales s{};
+    f32x4 t[4] = {};  // the first iteration scales nothing of one before
 #pragma unroll 1
-    for (int i = 0; i < I; ++i) iteration(a, b, s, i);
+    for (int i = 0; i < I; ++i) iteration(a, b, t, s, i);
+    scale<NP - 2>(t, s);
+    scale<NP - 1>(t, s);
     wait_vm<0>();  // the refills past the end
     lds_barrier();
   }
