@@ -40,7 +40,8 @@ from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  
                    skg_run_qknorm_rope, skg_run_qknorm_rope_bwd, skg_plan_run_qknorm_rope_bwd,
                    skg_qknorm_rope_bwd_workspace_bytes, skg_run_newton_schulz,
                    skg_newton_schulz_workspace_bytes, MODES,
-                   REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS, BLOCKS, ROPE_STYLES)
+                   REDUCTIONS, DTYPES, TILES, SCALE_MODES, SK_ORDERS, BLOCKS, ROPE_STYLES,
+                   NS_TILES)
 
 __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd", "plan_dgrad",
            "gemm_args", "wgrad_args", "conv_args",
@@ -55,7 +56,7 @@ __all__ = ["gemm", "wgrad", "fwd", "dgrad", "plan_gemm", "plan_wgrad", "plan_fwd
            "rmsnorm_args", "rmsnorm_bwd_args", "mx_args", "skg_run_rmsnorm",
            "skg_run_rmsnorm_bwd", "skg_plan_run_rmsnorm_bwd", "skg_rmsnorm_bwd_workspace_bytes",
            "skg_run_mx_quant",
-           "skg_run_mx_dequant", "BLOCKS", "ROPE_STYLES", "block_quant", "qknorm_rope",
+           "skg_run_mx_dequant", "BLOCKS", "ROPE_STYLES", "NS_TILES", "block_quant", "qknorm_rope",
            "qknorm_rope_bwd", "newton_schulz", "block_quant_args", "qknorm_rope_args",
            "newton_schulz_args", "skg_run_block_quant", "skg_run_qknorm_rope",
            "skg_run_qknorm_rope_bwd", "skg_plan_run_qknorm_rope_bwd",
@@ -84,6 +85,7 @@ _SCALE_MODE = _Names(SCALE_MODES, "scale mode")
 _SK_ORDER = _Names(SK_ORDERS, "stream-K order")
 _BLOCK = _Names(BLOCKS, "block shape")
 _STYLE = _Names(ROPE_STYLES, "rotation style")
+_NS_TILE = _Names(NS_TILES, "tile")
 
 
 def _ptr(t):
@@ -423,7 +425,7 @@ NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 def newton_schulz_args(g=None, out=None, *, rows, cols, dtype, dtype_out=None, steps=5,
                        coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, scale=1.0, ldg=None,
-                       ldo=None):
+                       ldo=None, tile="auto"):
     """``coefficients``: a, b, c for every step, or a row of three for each."""
     if coefficients and hasattr(coefficients[0], "__len__"):
         if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
@@ -439,7 +441,7 @@ def newton_schulz_args(g=None, out=None, *, rows, cols, dtype, dtype_out=None, s
         rows, cols, dt, dt if dtype_out is None else _DTYPE[dtype_out], steps,
         0 if g is None else g.data_ptr(), cols if ldg is None else ldg,
         0 if out is None else out.data_ptr(), cols if ldo is None else ldo,
-        ctypes.addressof(values), eps, scale)
+        ctypes.addressof(values), eps, scale, _NS_TILE[tile])
     a.keep = values  # the struct holds only their address
     return a
 

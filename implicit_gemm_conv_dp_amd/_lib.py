@@ -37,6 +37,8 @@ SCALE_MODES = {"rowcol": SCALE_ROWCOL, "tensor": SCALE_TENSOR, "mx": SCALE_MX_E8
 BLOCK_1x128, BLOCK_128x128 = 0, 1
 BLOCKS = {"1x128": BLOCK_1x128, "128x128": BLOCK_128x128}
 ROPE_HALF, ROPE_PAIRS = 0, 1
+NS_TILES = {"auto": -1, "32x32": 0, "64x64": 1, "128x128": 2, "192x192": 3, "256x192": 4,
+            "256x256": 5, "320x256": 6}
 ROPE_STYLES = {"half": ROPE_HALF, "pairs": ROPE_PAIRS}
 SK_ORDER_AUTO, SK_ORDER_BLOCK, SK_ORDER_XCD, SK_ORDER_KMAJOR = 0, 1, 2, 3
 SK_ORDERS = {"auto": SK_ORDER_AUTO, "block": SK_ORDER_BLOCK, "xcd": SK_ORDER_XCD,
@@ -156,7 +158,7 @@ class skg_newton_schulz_args_t(ctypes.Structure):
                 ("steps", ctypes.c_int32), ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
                 ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
                 ("coefficients", ctypes.c_void_p), ("eps", ctypes.c_float),
-                ("scale", ctypes.c_float)]
+                ("scale", ctypes.c_float), ("tile", ctypes.c_int32)]
 
 
 class skg_plan_t(ctypes.Structure):

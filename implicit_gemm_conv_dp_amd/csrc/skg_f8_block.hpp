@@ -246,8 +246,8 @@ struct F8Direct {
 };
 
 // --- many tiles ------------------------------------------------------------------
-// Eight waves on a ring of D stages, a stage a block of 128 of K; wave tile
-// TM/2 x TN/4 in 16 x 16 pieces.  Per stage a wave holds its columns' fragments and
+// Eight waves on a ring of D stages, a stage a block of 128 of K; a wave's part of
+// the tile in 16 x 16 pieces.  Per stage a wave holds its columns' fragments and
 // two of its rows', reads the next rows' while one's products run, and scales a
 // piece's results two instructions after they were started.
 //
@@ -255,8 +255,8 @@ struct F8Direct {
 // frees its slot, which stage i + D is loaded into, and the next stage's fragments
 // are read over the ones that the last row has done with.
 template <int TM_, int TN_, int D_, int FMT, bool ROWS, bool EXACT>
-struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> {
-  typedef Ring8<TM_, TN_, D_, (TM_ + TN_) * 4> R;
+struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4, TM_ == 2 * TN_ ? 4 : 2> {
+  typedef Ring8<TM_, TN_, D_, (TM_ + TN_) * 4, TM_ == 2 * TN_ ? 4 : 2> R;
   static constexpr int D = D_;
   using R::dst, R::step, R::I, R::lane, R::lds, R::na, R::nb, R::ra, R::rb, R::slot, R::wave, R::wm, R::wn, R::XOFF;
   static constexpr int TM = TM_, TN = TN_, WTM = R::WTM, WTN = R::WTN, RB = 128;

@@ -211,6 +211,241 @@ __global__ __launch_bounds__(256) void ns_direct_kernel(NsParams g) {
   T::run(g, (SKG_LDS char*)lds);
 }
 
+// --- many tiles ------------------------------------------------------------------
+// Eight waves on a ring of D stages of 64 elements of K, a wave's part of the tile in
+// 16 x 16 pieces.  A stage is 2 FM rows of FN instructions (two k-steps of 32); a row's
+// fragment of A is read AHEAD rows before it, a k-step's fragments of B in the rows
+// before.  AHEAD rows before its end a stage has been read: the barrier there frees
+// its slot, which stage i + D is loaded into, and the next stage's reads begin.
+template <int TM_, int TN_, int D_>
+struct NsRing : Ring8<TM_, TN_, D_, 0> {
+  typedef Ring8<TM_, TN_, D_, 0> R;
+  using R::dst, R::I, R::lane, R::lds, R::na, R::nb, R::ra, R::rb, R::slot, R::step, R::wave, R::wm, R::wn;
+  static constexpr int TM = TM_, TN = TN_, D = D_, WTM = R::WTM, WTN = R::WTN, RB = 128;
+  static constexpr int FM = WTM / 16, FN = WTN / 16, ROWS = 2 * FM, AHEAD = 3, NA = AHEAD + 1, PER = R::UA + R::UB;
+  static constexpr int STRIP = R::SLOT / 8;  // bytes of LDS of a wave's copy-out
+  static_assert(STRIP >= 32 * WTN * 4, "strips fit the slot");
+  static_assert(FM % 2 == 0 && ROWS % NA == 0 && FM > AHEAD, "rows");
+
+  uint32_t fra, frb;
+  f32x4 acc[FM][FN];
+
+  SKG_DEV NsRing(const NsParams& g, SKG_LDS char* l) {
+    R::init(l, g.lda_b, g.ldb_b, (g.K + 63) / 64);
+    const int r = lane & 15, q = lane >> 4;
+    fra = lds_off<RB>(wm * WTM + r, q);
+    frb = TM * RB + lds_off<RB>(wn * WTN + r, q);
+  }
+  SKG_DEV void open(const NsParams& g, int m0, int n0) {
+    ra = ring_rows(g.A, m0, g.M, g.lda_b, g.lda_b, na);
+    rb = ring_rows(g.B, n0, g.N, g.ldb_b, g.ldb_b, nb);
+  }
+  typedef i32x4 Frag;
+  // A lane's place in a slot at both k-steps: its chunk's number goes up by 4, an XOR
+  // within the permuted row.
+  struct At {
+    const SKG_LDS char* k[2];
+  };
+  SKG_DEV At at_k(uint32_t st, uint32_t first) const { return {{lds + (st + first), lds + ((st + first) ^ 64)}}; }
+  template <int ROW>
+  SKG_DEV static Frag read_a(const At& p) {
+    return *(const SKG_LDS Frag*)(p.k[ROW / FM] + ROW % FM * 16 * RB);
+  }
+  template <int N, int KSTEP>
+  SKG_DEV static Frag read_b(const At& p) {
+    return *(const SKG_LDS Frag*)(p.k[KSTEP] + N * 16 * RB);
+  }
+  SKG_DEV void iteration(Frag (&a)[NA], Frag (&b)[2][FN], int i) {
+    const uint32_t to = dst(0);
+    const At ca = at_k(slot(0), fra), cb = at_k(slot(0), frb);
+    At xa, xb;  // the next stage's
+    static_for<0, ROWS>([&](auto r_) {
+      constexpr int r = decltype(r_)::value, f = r % FM, ks = r / FM;
+      constexpr bool late = r >= ROWS - AHEAD;  // reads belong to the next stage
+      if constexpr (r == ROWS - AHEAD) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vm<(D - 2) * PER>();  // stage i + 1 has landed: the younger ones have not
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        xa = at_k(slot(1), fra);
+        xb = at_k(slot(1), frb);
+      }
+      static_for<0, FN>([&](auto n_) {
+        constexpr int n = decltype(n_)::value;
+        Mfma<DT_F16, 16>::run(acc[f][n], b[ks][n], a[r % NA]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (n == 0) {
+          // Row r + AHEAD goes where row r - 1 was.
+          if constexpr (late)
+            a[(r + AHEAD) % NA] = read_a<r + AHEAD - ROWS>(xa);
+          else
+            a[(r + AHEAD) % NA] = read_a<r + AHEAD>(ca);
+        }
+        // B of the second k-step in the first rows, of the next stage in the last.
+        if constexpr (late) {
+          constexpr int s = (r - (ROWS - AHEAD)) * FN + n;  // 0 .. AHEAD FN - 1
+          static_for<s * FN / (AHEAD * FN), (s + 1) * FN / (AHEAD * FN)>([&](auto m_) {
+            b[0][decltype(m_)::value] = read_b<decltype(m_)::value, 0>(xb);
+          });
+          static_for<s * PER / (AHEAD * FN), (s + 1) * PER / (AHEAD * FN)>([&](auto d_) {
+            R::template dma_rows<decltype(d_)::value>(i + D, to);
+          });
+        } else if constexpr (r >= 1 && r < 1 + FN && n == 1 % FN) {
+          b[1][r - 1] = read_b<r - 1, 1>(cb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    step();
+  }
+  SKG_DEV void ahead() {
+    static_for<0, D - 1>([&](auto j_) {
+      constexpr int j = decltype(j_)::value;
+      static_for<0, PER>([&](auto n_) { R::template dma_rows<decltype(n_)::value>(j, dst(j)); });
+    });
+  }
+  // acc = D beta / alpha, so that alpha acc is alpha A B^T + beta D at the end: D's
+  // loads travel with the first stages; behind a tile's stores they were waited for
+  // (40 us of a 4096 x 4096 product).  (D's rows are whole 128 bytes: columns come in
+  // fours.)
+  SKG_DEV void begin(const NsParams& g, int m0, int n0) {
+    const float ratio = g.beta / g.alpha;
+    const __amdgpu_buffer_rsrc_t rd =
+        make_rsrc_uniform(g.D + (int64_t)m0 * g.ldd * 2, (uint32_t)min((int64_t)max(g.M - m0, 0) * g.ldd * 2, (int64_t)0x7fffffff));
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      i32x2 d[FN];
+      const uint32_t row = (uint32_t)(wm * WTM + f * 16 + (lane & 15)) * (uint32_t)g.ldd;
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        const int c = n0 + wn * WTN + n * 16 + 4 * (lane >> 4);
+        d[n] = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(rd, c < g.cn ? (row + c) * 2 : kOOB, 0, 0));
+      }
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[f][n][e] = half_at(i32x4{d[n][0], d[n][1], 0, 0}, e) * ratio;
+    }
+  }
+  SKG_DEV void zero() {
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  SKG_DEV void mainloop() {
+    static_for<0, PER>([&](auto n_) { R::template dma_rows<decltype(n_)::value>(D - 1, dst(D - 1)); });
+    wait_vm<(D - 1) * PER>();
+    lds_barrier();
+    Frag a[NA], b[2][FN];
+    const At pa = at_k(slot(0), fra), pb = at_k(slot(0), frb);
+    static_for<0, AHEAD>([&](auto r_) { a[decltype(r_)::value] = read_a<decltype(r_)::value>(pa); });
+    static_for<0, FN>([&](auto n_) { b[0][decltype(n_)::value] = read_b<decltype(n_)::value, 0>(pb); });
+#pragma unroll 1
+    for (int i = 0; i < I; ++i) iteration(a, b, i);
+    wait_vm<0>();  // the refills past the end
+    lds_barrier();
+  }
+  // The wave's part of the tile, 32 rows at a time through LDS of its own, as they are
+  // and transposed.
+  template <int DT>
+  SKG_DEV void store_tile(const NsParams& g, int m0, int n0, bool diagonal, SKG_LDS char* strips) const {
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    SKG_LDS char* st = strips + wave * STRIP;
+    SKG_LDS char* tr = st + (DT == DT_F32 ? 0 : 32 * WTN * 2);  // fp32 (the last step's): one form only
+    const int r = lane & 15, q = lane >> 4, c0 = n0 + wn * WTN;
+    const bool transposed = g.Ct && !diagonal;
+    static_for<0, FM / 2>([&](auto h_) {
+      constexpr int h = decltype(h_)::value;
+      const int m = m0 + wm * WTM + h * 32;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          const f32x4 v = acc[2 * h + k][n] * g.alpha;
+          const int row = k * 16 + r;
+          if constexpr (DT == DT_F32) {
+            if (g.C) {
+              *(SKG_LDS f32x4*)(st + strip_off<4, WTN>(row, n * 4 + q)) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *(SKG_LDS float*)(tr + strip_off<4, 32>(n * 16 + 4 * q + e, row / 4) + (row & 3) * 4) = v[e];
+            }
+          } else {
+            const uint32_t p0 = ns_pack<DT>(v[0], v[1]), p1 = ns_pack<DT>(v[2], v[3]);
+            if (g.C) *(SKG_LDS i32x2*)(st + strip_off<2, WTN>(row, n * 2 + (q >> 1)) + (q & 1) * 8) = i32x2{(int)p0, (int)p1};
+            if (transposed) {
+              // Neighbouring lanes hold neighbouring rows: each takes one column's pair.
+              const uint32_t q0 = (uint32_t)__builtin_amdgcn_mov_dpp((int)p0, 0xB1, 0xf, 0xf, true);
+              const uint32_t q1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)p1, 0xB1, 0xf, 0xf, true);
+              const uint32_t w0 = r & 1 ? __builtin_amdgcn_perm(p0, q0, 0x07060302) : __builtin_amdgcn_perm(q0, p0, 0x05040100);
+              const uint32_t w1 = r & 1 ? __builtin_amdgcn_perm(p1, q1, 0x07060302) : __builtin_amdgcn_perm(q1, p1, 0x05040100);
+              const int col = n * 16 + 4 * q + (r & 1);
+              *(SKG_LDS uint32_t*)(tr + strip_off<2, 32>(col, row / 8) + (row % 8 / 2) * 4) = w0;
+              *(SKG_LDS uint32_t*)(tr + strip_off<2, 32>(col + 2, row / 8) + (row % 8 / 2) * 4) = w1;
+            }
+          }
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (g.C) store_strip<ES, WTN, 32>(st, g.C, g.ldc, m, c0, g.M, g.cn, g.vec);
+      if (transposed) store_strip<ES, 32, WTN>(tr, g.Ct, g.ldct, c0, m, g.N, g.ctn, g.vec);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    });
+  }
+};
+
+// The kernel's arguments, read again from memory where they are used between main
+// loops: kept in scalar registers through those, they would be spilled, along with
+// the resources of the direct-to-LDS loads.
+typedef const NsParams __attribute__((address_space(4))) * NsArgs;
+SKG_DEV const NsParams& ns_args() {
+  NsArgs p = (NsArgs)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const NsParams*)p;
+}
+
+template <class T>
+__global__ __launch_bounds__(512, 1) void ns_ring_kernel(NsParams first) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
+  T t(first, (SKG_LDS char*)lds);
+  TileRun run(first.tiles);
+  int k = run.k, tm, tn;
+  if (k >= run.count) return;
+  ns_tile(first, run.first + k, tm, tn);
+  t.open(first, tm * T::TM, tn * T::TN);
+  t.ahead();
+  for (;;) {
+    {
+      const NsParams& g = ns_args();
+      if (g.D)
+        t.begin(g, tm * T::TM, tn * T::TN);
+      else
+        t.zero();
+    }
+    t.mainloop();
+    // The next tile's first stages travel during this one's copy-out.
+    const NsParams& g = ns_args();
+    const int m = tm, n = tn;
+    k += run.per;
+    SKG_LDS char* last = (SKG_LDS char*)lds + t.slot(T::D - 1);  // the stage that ran last
+    if (k < run.count) {
+      ns_tile(g, run.first + k, tm, tn);
+      t.open(g, tm * T::TM, tn * T::TN);
+      t.ahead();
+    }
+    const bool diagonal = g.sym && m == n;
+    if (g.dt == DT_F16)
+      t.template store_tile<DT_F16>(g, m * T::TM, n * T::TN, diagonal, last);
+    else if (g.dt == DT_BF16)
+      t.template store_tile<DT_BF16>(g, m * T::TM, n * T::TN, diagonal, last);
+    else
+      t.template store_tile<DT_F32>(g, m * T::TM, n * T::TN, diagonal, last);
+    if (k >= run.count) return;
+    lds_barrier();  // every wave is done with the slot the strips went through
+  }
+}
+
 // --- the norm and the operands' first form ---------------------------------------
 constexpr int kSumBlocks = 512;
 struct NsInput {
@@ -318,16 +553,79 @@ int check_newton(const skg_newton_schulz_args_t* a) {
   if (a->steps < 1 || a->steps > SKG_NEWTON_SCHULZ_MAX_STEPS) return unsupported("steps must be 1 to SKG_NEWTON_SCHULZ_MAX_STEPS");
   if (a->ldg < a->cols || a->ldo < a->cols) return unsupported("leading dimension too small");
   if (!(a->eps >= 0.f)) return unsupported("eps must not be negative");
+  if (a->tile < SKG_NS_TILE_AUTO || a->tile >= SKG_NS_TILE_COUNT) return unsupported("unknown tile");
   if (!std::isfinite(a->scale)) return unsupported("scale must be finite");
   return SKG_OK;
 }
 
-hipError_t ns_product(NsParams p, hipStream_t st) {
-  typedef NsDirect<4, 4, 2> T;
-  p.tiles_m = (int)ceil_div(p.M, T::TM);
-  p.tiles_n = (int)ceil_div(p.N, T::TN);
-  p.tiles = p.sym ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
-  hipLaunchKernelGGL((ns_direct_kernel<T>), dim3((unsigned)p.tiles), dim3(256), 0, st, p);
+// Tiles of a product, over what is written of C and Ct (padding too); -1 where this
+// kernel does not take it: a symmetric one needs square tiles.
+int ns_tiles_m(const NsParams& p, int tm) { return (int)ceil_div(p.Ct ? std::max(p.M, p.ctn) : p.M, tm); }
+int ns_tiles_n(const NsParams& p, int tn) { return (int)ceil_div(p.C ? std::max(p.N, p.cn) : p.N, tn); }
+int ns_count(const NsParams& p, int tm, int tn) {
+  const int m = ns_tiles_m(p, tm), n = ns_tiles_n(p, tn);
+  return p.sym ? (tm == tn ? m * (m + 1) / 2 : -1) : m * n;
+}
+template <class T>
+void ns_launch(const NsParams& q, int cus, int threads, hipStream_t st, void (*kernel)(NsParams), bool walk) {
+  NsParams p = q;
+  p.tiles_m = ns_tiles_m(p, T::TM);
+  p.tiles_n = ns_tiles_n(p, T::TN);
+  p.tiles = ns_count(p, T::TM, T::TN);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(walk ? std::min(p.tiles, cus) : p.tiles)), dim3(threads), 0, st, p);
+}
+template <class T>
+void ns_ring(const NsParams& p, int cus, hipStream_t st) {
+  ns_launch<T>(p, cus, 512, st, ns_ring_kernel<T>, true);
+}
+template <class T>
+void ns_direct(const NsParams& p, int cus, hipStream_t st) {
+  ns_launch<T>(p, cus, 256, st, ns_direct_kernel<T>, false);
+}
+
+// The kernel and tile of a product: the least of the times that these models give, in
+// us, rounds x (start + stages x stage) of a workgroup a CU and the launch.  What counts
+// most for a large one is how full the last round is: 4096 x 4096 symmetric over 4864
+// 88 us on 192 x 192 (253 tiles; 105 on 256 x 256, 136 tiles; 123 on 128 x 128, 528
+// tiles), 4864 x 4096 over 4096 170 on 320 x 256 (256 tiles; 211 on 256 x 256, 304
+// tiles; 197 on 128 x 128).  The direct kernels' waves split K, which a small one
+// needs: fifteen products of 300 x 1111 and the norm take 101 us on 32 x 32, 143 on
+// 64 x 64 and 166 on 128 x 128, those of 1024 x 1024 237, 181 and 222.
+struct NsKernel {
+  int tm, tn, square;  // square: the kernel that takes this one's symmetric products
+  double launch, start, stage;
+  void (*run)(const NsParams&, int, hipStream_t);
+};
+const NsKernel kNsKernels[SKG_NS_TILE_COUNT] = {
+    /* 32x32   */ {32, 32, 0, 2, 1.2, 0.16, ns_direct<NsDirect<2, 2, 4>>},
+    /* 64x64   */ {64, 64, 1, 2, 3.3, 0.3, ns_direct<NsDirect<4, 4, 2>>},
+    /* 128x128 */ {128, 128, 2, 1, 5, 0.52, ns_ring<NsRing<128, 128, 4>>},
+    /* 192x192 */ {192, 192, 3, 1, 12, 0.97, ns_ring<NsRing<192, 192, 3>>},
+    /* 256x192 */ {256, 192, 3, 1, 16, 1.15, ns_ring<NsRing<256, 192, 2>>},
+    /* 256x256 */ {256, 256, 5, 1, 18, 1.3, ns_ring<NsRing<256, 256, 2>>},
+    /* 320x256 */ {320, 256, 5, 1, 26, 2.25, ns_ring<NsRing<320, 256, 2>>},
+};
+
+hipError_t ns_product(const NsParams& p, int tile, int cus, hipStream_t st) {
+  // A ring kernel divides D by alpha.
+  const bool rings = !p.D || std::fabs(p.alpha) > 1e-20f * std::fabs(p.beta);
+  if (tile == SKG_NS_TILE_AUTO) {
+    double best = 1e300;
+    for (int i = 0; i < SKG_NS_TILE_COUNT; ++i) {
+      const NsKernel& k = kNsKernels[i];
+      const int tiles = ns_count(p, k.tm, k.tn);
+      if (tiles <= 0 || (k.tm >= 128 && !rings)) continue;
+      const double us = k.launch + std::ceil((double)tiles / cus) * (k.start + (double)ceil_div(p.K, 64) * k.stage);
+      if (us < best) {
+        best = us;
+        tile = i;
+      }
+    }
+  } else {
+    if (p.sym) tile = kNsKernels[tile].square;
+    if (!rings && kNsKernels[tile].tm >= 128) tile = SKG_NS_TILE_64x64;
+  }
+  kNsKernels[tile].run(p, cus, st);
   return hipGetLastError();
 }
 
@@ -389,7 +687,7 @@ int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hip
     p.cn = p.ctn = (int)w.pm;
     p.alpha = kScaleS / (kScaleX * kScaleX);
     p.sym = 1;
-    e = ns_product(p, st);
+    e = ns_product(p, a->tile, cus, st);
     // P = b S + c S S
     p.A = p.B = p.D = s;
     p.lda_b = p.ldb_b = (uint32_t)w.pm * 2;
@@ -398,7 +696,7 @@ int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hip
     p.C = p.Ct = poly;
     p.alpha = cc * (kScaleP / (kScaleS * kScaleS));
     p.beta = cb * (kScaleP / kScaleS);
-    if (e == hipSuccess) e = ns_product(p, st);
+    if (e == hipSuccess) e = ns_product(p, a->tile, cus, st);
     // Y <- a Y + Y P, and X
     const bool last = i + 1 == a->steps;
     p.A = p.D = y;
@@ -428,7 +726,7 @@ int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hip
       p.alpha *= a->scale / kScaleX;
       p.beta *= a->scale / kScaleX;
     }
-    if (e == hipSuccess) e = ns_product(p, st);
+    if (e == hipSuccess) e = ns_product(p, a->tile, cus, st);
   }
   if (e != hipSuccess) return hip_failure(std::string("launch: ") + hipGetErrorString(e));
   return SKG_OK;

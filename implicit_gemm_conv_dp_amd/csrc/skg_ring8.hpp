@@ -1,5 +1,5 @@
-// Frame of the products that eight waves (2 x 4) of a workgroup compute on a ring
-// of direct-to-LDS stages: the stages' loads and the copy-out.
+// Frame of the products that eight waves (WM x 8 / WM) of a workgroup compute on a
+// ring of direct-to-LDS stages: the stages' loads and the copy-out.
 //
 // A stage is 128 bytes of K of the tile's TM rows of A, then of its TN rows of B,
 // then EXTRA bytes that the product adds.  Two waves a SIMD: one issues vector
@@ -12,10 +12,11 @@
 namespace skg {
 
 // Rows row0 .. rows-1 of an operand as a buffer that ends with the last one's
-// kbytes, so nothing past the operand is read.
+// kbytes, so nothing past the operand is read (nothing at all from row0 >= rows).
 SKG_DEV i32x4 ring_rows(const char* p, int row0, int rows, uint32_t pitch, uint32_t kbytes, int& n) {
   const uint64_t a = (uint64_t)(uintptr_t)(p + (size_t)row0 * pitch);
-  n = __builtin_amdgcn_readfirstlane((int)min((int64_t)(rows - row0 - 1) * pitch + kbytes, (int64_t)0x7fffffff));
+  const int64_t bytes = row0 < rows ? (int64_t)(rows - row0 - 1) * pitch + kbytes : 0;
+  n = __builtin_amdgcn_readfirstlane((int)min(bytes, (int64_t)0x7fffffff));
   return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(a >> 32)), n, 0x00020000};
 }
 // 16 (or 4) bytes a lane to LDS address dst + IMM, from a scalar offset soff of
@@ -36,31 +37,38 @@ SKG_DEV void ring_dma4(const i32x4& r, uint32_t dst, uint32_t voff, uint32_t sof
 }
 
 // NROWS rows of COLS elements of ES bytes in a wave's own LDS, in 16-byte pieces
-// that are XOR-permuted within a row.
+// that are rotated within a row by the row's number.
 template <int ES, int COLS>
 SKG_DEV uint32_t strip_off(int row, int piece) {
   constexpr int P = COLS * ES, CPR = P / 16;
-  return row * P + ((piece ^ row) % CPR) * 16;
+  return row * P + (uint32_t)(piece + row) % CPR * 16;
 }
 // Such a strip to rows m0 .. of C from column n0 on, whole 16-byte pieces where
 // `vec` (C and its pitch are aligned to them); M, N: where C ends.
 template <int ES, int COLS, int NROWS>
 SKG_DEV void store_strip(const SKG_LDS char* st, char* C, int64_t ldc, int m0, int n0, int M, int N, bool vec) {
-  constexpr int P = COLS * ES, CPR = P / 16, RPI = 64 / CPR, EC = 16 / ES;
-  static_assert(RPI <= NROWS && NROWS % RPI == 0, "strip");
+  constexpr int P = COLS * ES, CPR = P / 16, RPI = 64 / CPR < NROWS ? 64 / CPR : NROWS, EC = 16 / ES;
+  constexpr bool EVEN = RPI * CPR == 64 && NROWS % RPI == 0;  // every lane has a piece each time
   const int lane = threadIdx.x & 63, cc = lane % CPR, r0 = lane / CPR, col = n0 + cc * EC;
   char* o = C + ((int64_t)(m0 + r0) * ldc + col) * ES;
   const int64_t step = RPI * ldc * ES;
-  if (vec && m0 + NROWS <= M && n0 + COLS <= N) {
+  const bool fast = vec && m0 + NROWS <= M && n0 + COLS <= N;
+  if (EVEN && fast) {
 #pragma unroll
     for (int u = 0; u < NROWS / RPI; ++u)
       *(i32x4*)(o + u * step) = *(const SKG_LDS i32x4*)(st + strip_off<ES, COLS>(u * RPI + r0, cc));
+  } else if (fast) {
+#pragma unroll
+    for (int u = 0; u < (NROWS + RPI - 1) / RPI; ++u)
+      if (r0 < RPI && u * RPI + r0 < NROWS)
+        *(i32x4*)(o + u * step) = *(const SKG_LDS i32x4*)(st + strip_off<ES, COLS>(u * RPI + r0, cc));
   } else {
 #pragma unroll 1
-    for (int u = 0; u < NROWS / RPI; ++u) {
-      if (m0 + r0 + u * RPI >= M || col >= N) continue;
+    for (int u = 0; u < (NROWS + RPI - 1) / RPI; ++u) {
+      const int row = u * RPI + r0;
+      if (r0 >= RPI || row >= NROWS || m0 + row >= M || col >= N) continue;
       char* d = o + u * step;
-      const SKG_LDS char* q = st + strip_off<ES, COLS>(u * RPI + r0, cc);
+      const SKG_LDS char* q = st + strip_off<ES, COLS>(row, cc);
       if (vec && col + EC <= N) {
         *(i32x4*)d = *(const SKG_LDS i32x4*)q;
       } else {
@@ -76,10 +84,10 @@ SKG_DEV void store_strip(const SKG_LDS char* st, char* C, int64_t ldc, int m0, i
   }
 }
 
-template <int TM_, int TN_, int D_, int EXTRA_>
+template <int TM_, int TN_, int D_, int EXTRA_, int WM_ = 2>
 struct Ring8 {
   static constexpr int TM = TM_, TN = TN_, D = D_, RB = 128, THREADS = 512;
-  static constexpr int WTM = TM / 2, WTN = TN / 4;
+  static constexpr int WM = WM_, WN = 8 / WM, WTM = TM / WM, WTN = TN / WN;
   static constexpr int UA = TM / 64, UB = TN / 64;  // row DMAs a wave and stage
   static constexpr int EXTRA = EXTRA_, SLOT = (TM + TN) * RB + EXTRA;
   static constexpr int LDS = D * SLOT;
@@ -97,8 +105,8 @@ struct Ring8 {
     lds = l;
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    wm = wave >> 2;
-    wn = wave & 3;
+    wm = wave / WN;
+    wn = wave % WN;
     I = stages;
     at = 0;
     int row, chunk;

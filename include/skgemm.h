@@ -734,6 +734,20 @@ int skg_plan_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t 
  * fp16 factors make it).  G is read before out is written, so out may be G where
  * their types and pitches agree.  A matrix without elements writes nothing. */
 #define SKG_NEWTON_SCHULZ_MAX_STEPS 64
+/* The products' tiles.  AUTO picks each product's from its sizes; otherwise all take
+ * this one, but a symmetric product the square one of its width, and a step with
+ * c = 0 the 64x64 one for its polynomial. */
+enum skg_ns_tile {
+  SKG_NS_TILE_AUTO = -1,
+  SKG_NS_TILE_32x32 = 0,
+  SKG_NS_TILE_64x64 = 1,
+  SKG_NS_TILE_128x128 = 2,
+  SKG_NS_TILE_192x192 = 3,
+  SKG_NS_TILE_256x192 = 4,
+  SKG_NS_TILE_256x256 = 5,
+  SKG_NS_TILE_320x256 = 6,
+  SKG_NS_TILE_COUNT = 7
+};
 typedef struct skg_newton_schulz_args {
   int64_t rows, cols;
   int32_t dtype;           /* g: SKG_F16, SKG_BF16 or SKG_F32 */
@@ -745,6 +759,7 @@ typedef struct skg_newton_schulz_args {
   int64_t ldo;
   const float* coefficients;
   float eps, scale;
+  int32_t tile;            /* enum skg_ns_tile */
 } skg_newton_schulz_args_t;
 int skg_newton_schulz_workspace_bytes(const skg_newton_schulz_args_t* args, size_t* out);
 int skg_run_newton_schulz(const skg_newton_schulz_args_t* args, void* ws, size_t ws_bytes, void* stream);

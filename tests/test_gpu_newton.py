@@ -64,6 +64,41 @@ def test_update(rows, cols, dtype, dtype_out):
     check(run(g, rows, cols, dtype, dtype_out, pad=5), f64(g)[:, :cols], dtype_out)
 
 
+TILES = [t for t in skg.NS_TILES if t != "auto"]
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("rows,cols,dtype_out", [(200, 129, "bf16"), (129, 200, "f32"), (5, 3, "f16"), (700, 333, "f32"),
+                                                 (333, 700, "bf16"), (513, 512, "bf16")])
+def test_update_on_every_tile(tile, rows, cols, dtype_out):
+    pad = 0 if rows == 513 else 3
+    g = gradient(rows, rows, cols, "f32")
+    check(run(g, rows, cols, "f32", dtype_out, pad=pad, tile=tile), f64(g), dtype_out)
+
+
+@pytest.mark.parametrize("tile", ["auto"] + TILES)
+def test_cubic_steps(tile):
+    """c = 0: the polynomial is a multiple of S."""
+    cs = [(1.5, -0.5, 0.0)] * 6
+    g = gradient(14, 150, 210, "f32")
+    check(run(g, 150, 210, "f32", steps=6, coefficients=cs, tile=tile), f64(g), "f32", cs)
+
+
+def test_linear_steps():
+    """b = c = 0, and no product at all contributes."""
+    cs = [(1.25, 0.0, 0.0)] * 3
+    g = gradient(15, 64, 40, "f32")
+    check(run(g, 64, 40, "f32", steps=3, coefficients=cs), f64(g), "f32", cs)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_repeated_updates_give_the_same_bits(tile):
+    g = gradient(16, 400, 300, "f32")
+    first = run(g, 400, 300, "f32", tile=tile)
+    for _ in range(3):
+        assert np.array_equal(run(g, 400, 300, "f32", tile=tile), first)
+
+
 def test_aligned_output_of_large_update():
     g = gradient(7, 600, 520, "f32")
     check(run(g, 600, 520, "f32", "bf16"), f64(g), "bf16")

@@ -248,6 +248,8 @@ def update(ws=(0x10000, 1 << 40), **kw):
     (dict(steps=65), "steps"),
     (dict(ldg=95), "leading"),
     (dict(ldo=95), "leading"),
+    (dict(tile=7), "tile"),
+    (dict(tile=-2), "tile"),
     (dict(eps=-1.0), "eps"),
     (dict(eps=float("nan")), "eps"),
     (dict(scale=float("inf")), "scale"),
