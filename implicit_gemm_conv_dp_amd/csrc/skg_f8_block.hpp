@@ -30,24 +30,28 @@ struct F8Frag<FMT, false> {
 template <int FMT>
 struct F8Frag<FMT, true> {
   f16x8 v[4];
-  SKG_DEV void set(const i32x8& codes) {
+  // Codes 4 I .. 4 I + 3.
+  template <int I>
+  SKG_DEV void set_four(int codes) {
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f16x2 lo, hi;
-      if constexpr (FMT == 0) {
-        lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.f, false);
-        hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.f, true);
-      } else {
-        lo = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes[i], 1.f, false);
-        hi = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes[i], 1.f, true);
-      }
-      v[i / 2][i % 2 * 4] = lo[0];
-      v[i / 2][i % 2 * 4 + 1] = lo[1];
-      v[i / 2][i % 2 * 4 + 2] = hi[0];
-      v[i / 2][i % 2 * 4 + 3] = hi[1];
+    f16x2 lo, hi;
+    if constexpr (FMT == 0) {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.f, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.f, true);
+    } else {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes, 1.f, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes, 1.f, true);
     }
+    v[I / 2][I % 2 * 4] = lo[0];
+    v[I / 2][I % 2 * 4 + 1] = lo[1];
+    v[I / 2][I % 2 * 4 + 2] = hi[0];
+    v[I / 2][I % 2 * 4 + 3] = hi[1];
   }
+  template <int FIRST, int LAST>
+  SKG_DEV void set_part(const i32x8& codes) {
+    static_for<FIRST, LAST>([&](auto i_) { set_four<decltype(i_)::value>(codes[decltype(i_)::value]); });
+  }
+  SKG_DEV void set(const i32x8& codes) { set_part<0, 8>(codes); }
 };
 // Their products' sums over the block: element e of lane l is row l % 16 (of A),
 // column 4 (l / 16) + e (of B).
@@ -382,26 +386,78 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4, TM_ == 2 * TN_ ? 4 : 2> {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     const At na_ = rows_at(nxt, fra), nb_ = rows_at(nxt, frb);
-    i32x8 rb_[EXACT ? FN : 1];
     static_for<LAST, NP>([&](auto p_) {
       constexpr int p = decltype(p_)::value, n = p % FN;
       t[p % 4] = f8_block<FMT>(b[n], a[(FM - 1) & 1]);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (n == 0) raw = read<0>(na_);
-      if constexpr (EXACT)
-        rb_[n] = read<n>(nb_);
-      else
-        b[n].set(read<n>(nb_));
+      b[n].set(read<n>(nb_));
       static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + D, to); });
       scale<p - 2>(t, s);
       __builtin_amdgcn_sched_barrier(0);
     });
     a[0].set(raw);
-    if constexpr (EXACT) {
-#pragma unroll
-      for (int n = 0; n < FN; ++n) b[n].set(rb_[n]);
-    }
     __builtin_amdgcn_sched_barrier(0);
+    step();
+  }
+
+  // The same with fp16 fragments.  Their conversions cost the vector unit as much time
+  // as the matrix unit needs for the products, so they are spread between them: while
+  // a row's products run, the next row's codes are converted, and while the last
+  // row's run, the next stage's columns', each after its last product.  Codes
+  // holds them between their reads and their conversions.
+  struct Codes {
+    i32x8 a, b[2];
+  };
+  SKG_DEV void iteration_exact(Frag (&a)[2], Frag (&b)[FN], Codes& c, f32x4 (&t)[4], Scales& s, int i) {
+    const uint32_t cur = slot(0), nxt = slot(1), to = dst(0);
+    const At ca = rows_at(cur, fra), na_ = rows_at(nxt, fra), nb_ = rows_at(nxt, frb);
+    static_for<0, NP>([&](auto p_) {
+      constexpr int p = decltype(p_)::value, f = p / FN, n = p % FN;
+      constexpr bool last = f == FM - 1;
+      if constexpr (p == LAST) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vm<(D - 2) * PER>();  // stage i + 1 has landed: the younger ones have not
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        c.a = read<0>(na_);
+        c.b[0] = read<0>(nb_);
+      }
+      f32x4& r = t[p % 4];
+      r = f32x4{0.f, 0.f, 0.f, 0.f};
+      static_for<0, 4>([&](auto h_) {
+        constexpr int h = decltype(h_)::value;
+        r = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[n].v[h], a[f & 1].v[h], r, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        // Row f + 1: over all of this row's pieces, over the later ones in the last row.
+        constexpr int from = last ? 1 : 0, steps = 4 * (FN - from), k = 4 * (n - from) + h;
+        if constexpr (k >= 0) a[(f + 1) & 1].template set_part<k * 8 / steps, (k + 1) * 8 / steps>(c.a);
+        // The columns' next stage, the last of them in the next stage's first piece.
+        if constexpr (last && n > 0) b[n - 1].template set_part<2 * h, 2 * h + 2>(c.b[(n - 1) & 1]);
+        if constexpr (p == 0) b[FN - 1].template set_part<2 * h, 2 * h + 2>(c.b[(FN - 1) & 1]);
+        if constexpr (h == 3 && last && n + 1 < FN) c.b[(n + 1) & 1] = read<n + 1>(nb_);
+        if constexpr (h == 1) {
+          if constexpr (p == 2 && !ROWS) {
+#pragma unroll
+            for (int f_ = 0; f_ < FM; ++f_) s.a[f_] *= s.b[0][0];
+          }
+          if constexpr (p >= 2)
+            scale<p - 2>(t, s);
+          else
+            scale<NP - 2 + p>(t, s);
+          if constexpr (p == 1) read_scales(s, cur);
+        }
+        if constexpr (h == 3 && n == FN - 1) {
+          if constexpr (f + 2 < FM)
+            c.a = read<f + 2>(ca);
+          else if constexpr (last)
+            c.a = read<1>(na_);
+        }
+        if constexpr (h == 2 && last)
+          static_for<(p - LAST) * PER / FN, (p - LAST + 1) * PER / FN>([&](auto d_) { dma<decltype(d_)::value>(i + D, to); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
     step();
   }
 
@@ -426,8 +482,16 @@ struct F8Ring : Ring8<TM_, TN_, D_, (TM_ + TN_) * 4, TM_ == 2 * TN_ ? 4 : 2> {
     static_for<0, FN>([&](auto n_) { b[decltype(n_)::value].set(read<decltype(n_)::value>(bt)); });
     Scales s{};
     f32x4 t[4] = {};  // the first iteration scales nothing of one before
+    if constexpr (EXACT) {
+      Codes c;
+      c.a = read<1>(rows_at(slot(0), fra));
+      c.b[(FN - 1) & 1] = read<FN - 1>(bt);
 #pragma unroll 1
-    for (int i = 0; i < I; ++i) iteration(a, b, t, s, i);
+      for (int i = 0; i < I; ++i) iteration_exact(a, b, c, t, s, i);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < I; ++i) iteration(a, b, t, s, i);
+    }
     scale<NP - 2>(t, s);
     scale<NP - 1>(t, s);
     wait_vm<0>();  // the refills past the end
