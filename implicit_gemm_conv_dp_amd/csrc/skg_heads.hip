@@ -89,6 +89,8 @@ SKG_DEV void load_floats(float (&v)[N], const float* p) {
 struct Turn {
   float c[8], s[8];
 };
+// PLAIN: see heads_bwd_kernel.
+template <bool PLAIN>
 SKG_DEV Turn load_turn(const HeadsParams& p, uint32_t token, int e0) {
   Turn r;
 #pragma unroll
@@ -108,7 +110,7 @@ SKG_DEV Turn load_turn(const HeadsParams& p, uint32_t token, int e0) {
   const float* cs = p.cos + (known ? pos : 0) * p.half;
   const float* sn = p.sin + (known ? pos : 0) * p.half;
   if (p.pairs) {
-    if ((p.half & 3) == 0) {  // a lane's four pairs all are, or none is, turned
+    if (PLAIN || (p.half & 3) == 0) {  // a lane's four pairs all are, or none is, turned
       if (e0 < 2 * p.half) {
         float c[4], s[4];
         load_floats<4>(c, cs + e0 / 2);
@@ -128,7 +130,7 @@ SKG_DEV Turn load_turn(const HeadsParams& p, uint32_t token, int e0) {
         }
     }
   } else {
-    if ((p.half & 7) == 0) {  // a lane's eight elements lie on one side
+    if (PLAIN || (p.half & 7) == 0) {  // a lane's eight elements lie on one side
       if (e0 < 2 * p.half) {
         const bool low = e0 < p.half;
         load_floats<8>(r.c, cs + (low ? e0 : e0 - p.half));
@@ -157,6 +159,7 @@ SKG_DEV Turn load_turn(const HeadsParams& p, uint32_t token, int e0) {
 // Turns a lane's elements; `row` is LDS of the group, a float for each element.
 // Only the group's own wave touches it, so the wave's order of its LDS accesses
 // is enough; the fences keep the compiler to it.
+template <bool PLAIN>
 SKG_DEV void turn(float (&v)[8], const Turn& r, const HeadsParams& p, int e0, SKG_LDS float* row) {
   float m[8];
   if (p.pairs) {
@@ -167,7 +170,7 @@ SKG_DEV void turn(float (&v)[8], const Turn& r, const HeadsParams& p, int e0, SK
     *(SKG_LDS f32x4*)(row + e0) = f32x4{v[0], v[1], v[2], v[3]};
     *(SKG_LDS f32x4*)(row + e0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
     asm volatile("" ::: "memory");
-    if ((p.half & 7) == 0) {
+    if (PLAIN || (p.half & 7) == 0) {
       const int o = e0 < p.half ? e0 + p.half : e0 < 2 * p.half ? e0 - p.half : e0;
       const f32x4 a = *(const SKG_LDS f32x4*)(row + o), b = *(const SKG_LDS f32x4*)(row + o + 4);
 #pragma unroll
@@ -185,7 +188,8 @@ SKG_DEV void turn(float (&v)[8], const Turn& r, const HeadsParams& p, int e0, SK
     asm volatile("" ::: "memory");
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = e0 + j < 2 * p.half ? __builtin_fmaf(m[j], r.s[j], v[j] * r.c[j]) : v[j];
+  for (int j = 0; j < 8; ++j)
+    v[j] = (PLAIN ? e0 : e0 + j) < 2 * p.half ? __builtin_fmaf(m[j], r.s[j], v[j] * r.c[j]) : v[j];
 }
 
 template <class C>
@@ -209,7 +213,7 @@ SKG_DEV void heads_rows(const HeadsParams& p, SKG_LDS float* lds) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
     x[u] = load_within<DT, TAIL>(reinterpret_cast<const raw*>(head_at(s.x, s.sx, b, t, min(h0 + u, s.heads - 1), ES)), e0, p.D);
-  const Turn r = load_turn(p, token, e0);
+  const Turn r = load_turn<false>(p, token, e0);
   float w[8];
   head_weights<DT, TAIL>(w, s, p, e0);
 #pragma unroll
@@ -224,7 +228,7 @@ SKG_DEV void heads_rows(const HeadsParams& p, SKG_LDS float* lds) {
     const float f = rsqrt_refined(lanes_reduce<OpSum, LANES>(sum) * p.inv_d + p.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = v[j] * f * w[j];
-    turn(v, r, p, e0, lds + sub * LANES * 8);
+    turn<false>(v, r, p, e0, lds + sub * LANES * 8);
     Chunk<DT> c;
 #pragma unroll
     for (int j = 0; j < 8; ++j) c.put(j, v[j]);
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(kHeadThreads) void heads_kernel(HeadsParams p) {
 // The groups of a workgroup walk their shares in steps of the whole launch and
 // add up dw of their elements; at the end the groups' sums are added in a fixed
 // order through LDS.
-template <int DT, int LANES, int U, int TAIL>
+template <int DT, int LANES, int U, int TAIL, bool PLAIN>
 SKG_DEV void heads_bwd_rows(const HeadsParams& p, SKG_LDS float* lds) {
   typedef typename Elem<DT>::raw raw;
   constexpr int GROUPS = kHeadThreads / LANES, ES = sizeof(raw);
@@ -268,7 +272,7 @@ SKG_DEV void heads_bwd_rows(const HeadsParams& p, SKG_LDS float* lds) {
       x[u] = load_within<DT, TAIL>(reinterpret_cast<const raw*>(head_at(s.x, s.sx, b, t, h, ES)), e0, p.D);
       dy[u] = load_within<DT, TAIL>(reinterpret_cast<const raw*>(head_at(s.dy, s.sdy, b, t, h, ES)), e0, p.D);
     }
-    Turn r = load_turn(p, token, e0);
+    Turn r = load_turn<PLAIN>(p, token, e0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) r.s[j] = -r.s[j];
 #pragma unroll
@@ -279,7 +283,7 @@ SKG_DEV void heads_bwd_rows(const HeadsParams& p, SKG_LDS float* lds) {
       float g[8], sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = dy[u].get(j);
-      turn(g, r, p, e0, lds + sub * LANES * 8);
+      turn<PLAIN>(g, r, p, e0, lds + sub * LANES * 8);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = x[u].get(j);
@@ -312,12 +316,21 @@ SKG_DEV void heads_bwd_rows(const HeadsParams& p, SKG_LDS float* lds) {
     s.partial[(int64_t)block * p.D + e] = sum;
   }
 }
-template <int DT, int LANES, int U>
-__global__ __launch_bounds__(kHeadThreads) void heads_bwd_kernel(HeadsParams p) {
+// PLAIN: whole chunks of eight elements, each of which is turned as one or not at
+// all, by eight (or, of neighbours, four) table entries in a row.  A kernel of its
+// own, so that its four workgroups a CU, with two heads a group, stay resident:
+// 16384 x (32 + 8) x 128 bf16 106 us, 119 with the others' registers and four heads.
+// (The forward pass is not faster for it.)
+template <int DT, int LANES, int U, bool PLAIN>
+__global__ __launch_bounds__(kHeadThreads, PLAIN ? 4 : 1) void heads_bwd_kernel(HeadsParams p) {
   __shared__ __attribute__((aligned(16))) float lds[kHeadThreads * 8];
-  if (!(p.D & 7)) return heads_bwd_rows<DT, LANES, U, 0>(p, (SKG_LDS float*)lds);
-  if (p.D >= 8) return heads_bwd_rows<DT, LANES, U, 1>(p, (SKG_LDS float*)lds);
-  if constexpr (LANES == 8) heads_bwd_rows<DT, LANES, U, 2>(p, (SKG_LDS float*)lds);
+  if constexpr (PLAIN) {
+    heads_bwd_rows<DT, LANES, U, 0, true>(p, (SKG_LDS float*)lds);
+  } else {
+    if (!(p.D & 7)) return heads_bwd_rows<DT, LANES, U, 0, false>(p, (SKG_LDS float*)lds);
+    if (p.D >= 8) return heads_bwd_rows<DT, LANES, U, 1, false>(p, (SKG_LDS float*)lds);
+    if constexpr (LANES == 8) heads_bwd_rows<DT, LANES, U, 2, false>(p, (SKG_LDS float*)lds);
+  }
 }
 
 // dw of queries (blockIdx.y 0) and keys: the workgroups' partial sums in a fixed
@@ -360,10 +373,10 @@ bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 
 int lanes_of(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
-// Heads of one token that a group takes: several where that leaves enough groups
-// to fill the device.
-int heads_a_group(int64_t tokens, int heads, int lanes) {
-  return tokens * ceil_div(heads, 4) * lanes >= int64_t(64) * 4096 ? 4 : 1;
+// Heads of one token that a group takes: most of them where that leaves enough
+// groups to fill the device.
+int heads_a_group(int64_t tokens, int heads, int lanes, int most) {
+  return tokens * ceil_div(heads, most) * lanes >= int64_t(64) * 4096 ? most : 1;
 }
 // Shares of queries or keys: heads in fours (or one by one) for each token.
 int64_t shares(int64_t tokens, int heads, int u) { return tokens * ceil_div(heads, u); }
@@ -376,7 +389,7 @@ HeadPlan plan_heads(const skg_heads_args_t* a, bool bwd) {
   HeadPlan p;
   p.lanes = lanes_of(a->head_dim);
   const int64_t tokens = a->batch * a->seq;
-  p.u = heads_a_group(tokens, std::max(a->heads_q, a->heads_k), p.lanes);
+  p.u = heads_a_group(tokens, std::max(a->heads_q, a->heads_k), p.lanes, bwd ? 2 : 4);
   const int groups = kHeadThreads / p.lanes;
   for (int i = 0; i < 2; ++i) {
     p.items[i] = shares(tokens, i ? a->heads_k : a->heads_q, p.u);
@@ -456,13 +469,21 @@ int fill_heads(const skg_heads_args_t* a, const HeadPlan& pl, HeadsParams& p) {
   return SKG_OK;
 }
 
-template <class F>
-void by_heads(int dtype, const HeadPlan& pl, F&& f) {
-  auto by_u = [&](auto dt, auto lanes) {
-    if (pl.u == 4)
-      f(dt, lanes, std::integral_constant<int, 4>{});
+template <int U, class F>
+void by_heads(const skg_heads_args_t* a, const HeadPlan& pl, F&& f) {
+  const int dtype = a->dtype;
+  const bool plain = a->head_dim % 8 == 0 && a->rope_dim % (a->style == SKG_ROPE_PAIRS ? 8 : 16) == 0;
+  auto by_plain = [&](auto dt, auto lanes, auto u) {
+    if (plain)
+      f(dt, lanes, u, std::true_type{});
     else
-      f(dt, lanes, std::integral_constant<int, 1>{});
+      f(dt, lanes, u, std::false_type{});
+  };
+  auto by_u = [&](auto dt, auto lanes) {
+    if (pl.u == U)
+      by_plain(dt, lanes, std::integral_constant<int, U>{});
+    else
+      by_plain(dt, lanes, std::integral_constant<int, 1>{});
   };
   auto by_lanes = [&](auto dt) {
     if (pl.lanes == 8)
@@ -502,7 +523,7 @@ int run_heads(const skg_heads_args_t* a, hipStream_t st) {
   p.set[0].sy = {a->yq_strides.batch, a->yq_strides.token, a->yq_strides.head};
   p.set[1].y = static_cast<char*>(a->yk);
   p.set[1].sy = {a->yk_strides.batch, a->yk_strides.token, a->yk_strides.head};
-  by_heads(a->dtype, pl, [&](auto dt, auto lanes, auto u) {
+  by_heads<4>(a, pl, [&](auto dt, auto lanes, auto u, auto) {
     hipLaunchKernelGGL((heads_kernel<decltype(dt)::value, decltype(lanes)::value, decltype(u)::value>),
                        dim3((unsigned)blocks), dim3(kHeadThreads), 0, st, p);
   });
@@ -565,8 +586,8 @@ int run_heads_bwd(const skg_heads_args_t* a, void* ws, size_t ws_bytes, hipStrea
   if (rc) return rc;
   hipError_t e;
   if (blocks) {
-    by_heads(a->dtype, pl, [&](auto dt, auto lanes, auto u) {
-      hipLaunchKernelGGL((heads_bwd_kernel<decltype(dt)::value, decltype(lanes)::value, decltype(u)::value>), dim3(blocks),
+    by_heads<2>(a, pl, [&](auto dt, auto lanes, auto u, auto plain) {
+      hipLaunchKernelGGL((heads_bwd_kernel<decltype(dt)::value, decltype(lanes)::value, decltype(u)::value, decltype(plain)::value>), dim3(blocks),
                          dim3(kHeadThreads), 0, st, p);
     });
     e = hipGetLastError();

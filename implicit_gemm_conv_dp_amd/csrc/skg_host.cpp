@@ -412,7 +412,7 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
 // one of its four waves takes (the latency of the loads), one more workgroup on each CU
 // `more` and `each` (their rate).  A ring kernel's round costs `more` and `each` a stage.
 // An fp32 output's stages cost nearly twice (its matrix instructions are fp16's), and
-// 256 x 256 has no registers for them; a scale a column costs another 15 %.
+// 256 x 256 has no registers for them; a scale a column costs another 8 to 15 %.
 //
 //                       16x16   16x32   32x32   32x64   64x64   128x128  256x128  256x256
 //   1 x 4096 x 4096       5.8     6.5     7.4     9.8    12.8     19.2     27.8     47.0
@@ -445,8 +445,9 @@ static int resolve_block_tile(const skg_gemm_args_t& r) {
       const double blocks = (double)ceil_div(r.K, 512);
       us = 1.5 + std::max(m.start + m.block * blocks, rounds * (m.more + m.each * blocks));
     } else {
-      const double each = exact ? (t.tm == 256 ? 1.8 : 1.05) : m.each * (r.scale_mode == SKG_SCALE_ROW128 ? 1.15 : 1);
-      us = 1 + rounds * (m.more + each * (double)ceil_div(r.K, 128));
+      const double rows = r.scale_mode != SKG_SCALE_ROW128 ? 1 : exact ? 1.08 : 1.15;
+      const double each = exact ? (t.tm == 256 ? 1.6 : 1.05) : m.each;
+      us = 1 + rounds * (m.more + each * rows * (double)ceil_div(r.K, 128));
     }
     if (us < best) {
       best = us;
