@@ -7,7 +7,7 @@
 // bound), the even one of two.  16-bit inputs often lie just between two codes
 // (x MAX is exact in fp32), so the quotient is rounded correctly before it is
 // rounded to a code: a reciprocal and one residual step, four operations an
-// element, which memory traffic hides.
+// element.
 //
 // A workgroup takes 128 x 128 elements, from one read for every output that is
 // asked for: the rows' codes go straight from registers, the columns' by way of
@@ -41,7 +41,10 @@ SKG_DEV Quotient block_quotient(uint32_t top) {
   constexpr float MAX = E5M2 ? 57344.f : 448.f;
   Quotient r;
   const float m = from_bits(top);
-  r.d = m / MAX;
+  // m / MAX, rounded correctly (checked for every fp32 m of this branch's range).
+  constexpr float INV = 1.f / MAX;
+  const float over = m * INV;
+  r.d = __builtin_fmaf(__builtin_fmaf(-over, MAX, m), INV, over);
   if (m < MAX * 0x1p-126f) {
     r.d = 0x1p-126f;
     r.a = 0x1p+126f;
@@ -53,7 +56,9 @@ SKG_DEV Quotient block_quotient(uint32_t top) {
     const float p = from_bits(e >= 254 ? 0x00400000u : (254u - e) << 23);
     r.a = MAX * p;
     r.t = m * p;
-    r.inv = 1.f / r.t;
+    // To 2^-24: a code's quotient takes a residual step, which squares the error.
+    const float inv = __builtin_amdgcn_rcpf(r.t);
+    r.inv = __builtin_fmaf(__builtin_fmaf(-r.t, inv, 1.f), inv, inv);
   }
   // An infinity or NaN makes the whole block NaN.
   if (top >= 0x7f800000u) r.a = r.d = __builtin_nanf("");
@@ -77,6 +82,29 @@ SKG_DEV uint2 pack_codes(const float (&v)[8]) {
     hi = __builtin_amdgcn_cvt_pk_bf8_f32(v[4], v[5], hi, false);
     hi = __builtin_amdgcn_cvt_pk_bf8_f32(v[6], v[7], hi, true);
     return make_uint2((uint32_t)lo, (uint32_t)hi);
+  }
+}
+// The largest magnitude of eight elements, as fp32 bits; 16-bit ones are compared
+// as they are, two at a time.
+template <int DT>
+SKG_DEV uint32_t top_bits(const Chunk<DT>& c) {
+  if constexpr (DT == DT_F32) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = OpMaxBits::op(m, abs_bits(c.get(j)));
+    return m;
+  } else {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    struct Words {
+      uint32_t w[4];
+    };
+    const Words u = __builtin_bit_cast(Words, c);
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, u.w[i] & 0x7fff7fffu));
+    Chunk<DT> top;
+    top.v[0] = __builtin_bit_cast(typename Elem<DT>::raw, (uint16_t)(m[0] > m[1] ? m[0] : m[1]));
+    return abs_bits(top.get(0));
   }
 }
 template <int DT, bool E5M2>
@@ -124,9 +152,7 @@ SKG_DEV void block_tile(const BlockParams& p, SKG_LDS char* tile, SKG_LDS uint32
     const int k = u * T::THREADS + threadIdx.x, r = k / 16, g = k % 16 * 2;
     place_chunk<DT, TAIL>(in[u], (int)c0 + g * 4, (int)p.cols);
     if (r0 + r >= p.rows) in[u] = Chunk<DT>{};
-    top[u] = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top[u] = OpMaxBits::op(top[u], abs_bits(in[u].get(j)));
+    top[u] = top_bits(in[u]);
     if constexpr (TALL)
       all = OpMaxBits::op(all, top[u]);
     else
@@ -188,10 +214,7 @@ SKG_DEV void block_tile(const BlockParams& p, SKG_LDS char* tile, SKG_LDS uint32
       if constexpr (TALL) {
         o = whole;
       } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = OpMaxBits::op(m, abs_bits(v[j].get(i)));
-        o = block_quotient<E5M2>(lanes_reduce<OpMaxBits, 16>(m));
+        o = block_quotient<E5M2>(lanes_reduce<OpMaxBits, 16>(top_bits(v[j])));
       }
       if (line < p.cols && k0 < p.kqt) {
         store_loose(p.qt + line * p.ldqt + k0, block_codes<DT, E5M2>(v[j], o));
