@@ -117,6 +117,22 @@ struct NsDirect {
         ring_dma16<n * 1024>(a, dst, offa[n & 1] + n * 8 * g.lda_b, kb);
       });
     };
+    // The wave's fragments of the joined tile, and D there, which travels with the
+    // first stages (its rows are padded: whole fours).
+    constexpr int PART = (FM * FN + WAVES - 1) / WAVES;
+    auto place = [&](int k, int& m, int& n) {
+      const int f = k * WAVES + wave;
+      m = m0 + f / FN * 16 + (lane & 15);
+      n = n0 + f % FN * 16 + 4 * (lane >> 4);
+      return f < FM * FN;
+    };
+    uint2 d[PART];
+#pragma unroll
+    for (int k = 0; k < PART; ++k) {
+      int m, n;
+      d[k] = make_uint2(0, 0);
+      if (place(k, m, n) && g.D && m < g.M && n < g.cn) d[k] = *(const uint2*)(g.D + ((int64_t)m * g.ldd + n) * 2);
+    }
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -161,22 +177,17 @@ struct NsDirect {
       for (int j = 0; j < FN; ++j) red[(wave * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < (FM * FN + WAVES - 1) / WAVES; ++k) {
+    for (int k = 0; k < PART; ++k) {
+      int m, n;
+      if (!place(k, m, n)) break;
       const int f = k * WAVES + wave;
-      if (f >= FM * FN) break;
       f32x4 v = red[f * 64 + lane];
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) v += red[(w * FM * FN + f) * 64 + lane];
-      const int m = m0 + f / FN * 16 + (lane & 15), n = n0 + f % FN * 16 + 4 * (lane >> 4);
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (g.D && m < g.M && n < g.cn) {  // D's rows are padded: whole fours
-        const uint2 d = *(const uint2*)(g.D + ((int64_t)m * g.ldd + n) * 2);
-        const i32x4 w = {(int)d.x, (int)d.y, 0, 0};
+      const i32x4 w = {(int)d[k].x, (int)d[k].y, 0, 0};
+      float x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = half_at(w, e);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(v[e], g.alpha, x[e] * g.beta);
+      for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(v[e], g.alpha, half_at(w, e) * g.beta);
       auto put = [&](char* base, int64_t at, float y) {
         if (g.dt == DT_F32)
           ((float*)base)[at] = y;
@@ -447,34 +458,50 @@ __global__ __launch_bounds__(512, 1) void ns_ring_kernel(NsParams first) {
 }
 
 // --- the norm and the operands' first form ---------------------------------------
-constexpr int kSumBlocks = 512;
+constexpr int kSumBlocks = 1024;
 struct NsInput {
   const char* g;
   int64_t rows, cols, ldg;
   double* partial;
   char *x, *xt;      // G / norm as it lies (rows x cols) and transposed
   int64_t px, pxt;   // their pitches in elements
+  uint32_t chunks;   // of eight elements: rows x per
+  FastDiv per;
+  FastDiv across;    // tiles of 64 columns
   float eps;
   int blocks;
 };
+// Elements c .. c + 7 of a row, zeros past its end.
+template <int DT>
+SKG_DEV Chunk<DT> ns_load(const NsInput& a, int64_t row, int64_t c) {
+  const typename Elem<DT>::raw* p = reinterpret_cast<const typename Elem<DT>::raw*>(a.g) + row * a.ldg + c;
+  if (c + 8 <= a.cols) return reinterpret_cast<const Loose<Chunk<DT>>*>(p)->c;
+  Chunk<DT> v{};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < a.cols) v.v[j] = p[j];
+  return v;
+}
+// Four chunks of a thread's are on their way at once (4864 x 4096 fp32: 16 us; one at a
+// time 23).
 template <int DT>
 __global__ __launch_bounds__(256) void ns_sum_kernel(NsInput a) {
-  typedef typename Elem<DT>::raw raw;
+  constexpr int U = 4;
   __shared__ double part[4];
   double sum = 0;
-  const raw* g = reinterpret_cast<const raw*>(a.g);
-  const uint32_t per = (uint32_t)((a.cols + 7) / 8);  // chunks a row
-  const int64_t all = a.rows * (int64_t)per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per;
-    const int c = (int)(i - r * per) * 8, n = (int)min((int64_t)8, a.cols - c);
-    const raw* p = g + r * a.ldg + c;
-    if (n == 8) {
-      const Chunk<DT> v = reinterpret_cast<const Loose<Chunk<DT>>*>(p)->c;
+  const uint32_t step = gridDim.x * 256;
+  for (uint64_t i = blockIdx.x * 256 + threadIdx.x; i < a.chunks; i += (uint64_t)U * step) {
+    Chunk<DT> v[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)v.get(j), (double)v.get(j), sum);
-    } else {
-      for (int j = 0; j < n; ++j) sum = __builtin_fma((double)Elem<DT>::get(p[j]), (double)Elem<DT>::get(p[j]), sum);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t k = (uint32_t)min(i + (uint64_t)u * step, (uint64_t)a.chunks - 1), r = fdiv(k, a.per);
+      v[u] = ns_load<DT>(a, r, (int64_t)(k - r * a.per.d) * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + (uint64_t)u * step >= a.chunks) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)v[u].get(j), (double)v[u].get(j), sum);
     }
   }
 #pragma unroll
@@ -483,12 +510,20 @@ __global__ __launch_bounds__(256) void ns_sum_kernel(NsInput a) {
   __syncthreads();
   if (threadIdx.x == 0) a.partial[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
-// Tiles of 64 x 64: both forms, their padding with zeros.
+// Tiles of 64 x 64: both forms, their padding with zeros, in whole 128-byte rows.
 template <int DT>
 __global__ __launch_bounds__(256) void ns_first_kernel(NsInput a) {
-  typedef typename Elem<DT>::raw raw;
   __shared__ double part[4];
-  __shared__ uint16_t tile[64][66];
+  __shared__ uint32_t tile[64][33];
+  const uint32_t down = fdiv(blockIdx.x, a.across);
+  const int64_t r0 = (int64_t)down * 64, c0 = (int64_t)(blockIdx.x - down * a.across.d) * 64;
+  const int chunk = threadIdx.x & 7, line = threadIdx.x >> 3;  // of 32 lines
+  Chunk<DT> v[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t r = r0 + u * 32 + line;
+    v[u] = ns_load<DT>(a, min(r, a.rows - 1), c0 + chunk * 8);
+  }
   double sum = 0;
   for (int i = threadIdx.x; i < a.blocks; i += 256) sum += a.partial[i];
 #pragma unroll
@@ -496,18 +531,36 @@ __global__ __launch_bounds__(256) void ns_first_kernel(NsInput a) {
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
   __syncthreads();
   const double f = (double)kScaleX / (__builtin_sqrt(part[0] + part[1] + part[2] + part[3]) + (double)a.eps);
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const raw* g = reinterpret_cast<const raw*>(a.g);
-  const int c = threadIdx.x & 63;
-  for (int i = threadIdx.x >> 6; i < 64; i += 4) {
-    uint16_t h = 0;
-    if (r0 + i < a.rows && c0 + c < a.cols) h = to_f16_bits((float)((double)Elem<DT>::get(g[(r0 + i) * a.ldg + c0 + c]) * f));
-    tile[i][c] = h;
-    if (r0 + i < a.rows) reinterpret_cast<uint16_t*>(a.x)[(r0 + i) * a.px + c0 + c] = h;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t r = r0 + u * 32 + line;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = to_f16_bits((float)((double)v[u].get(2 * j) * f)), hi = to_f16_bits((float)((double)v[u].get(2 * j + 1) * f));
+      w[j] = lo | hi << 16;
+      // Zeros where nothing is read (a zero times an infinite factor is none).
+      if (r >= a.rows || c0 + chunk * 8 + 2 * j >= a.cols)
+        w[j] = 0;
+      else if (c0 + chunk * 8 + 2 * j + 1 >= a.cols)
+        w[j] &= 0xffff;
+      tile[u * 32 + line][chunk * 4 + j] = w[j];
+    }
+    if (r < a.rows) *(uint4*)(a.x + (r * a.px + c0 + chunk * 8) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncthreads();
-  for (int i = threadIdx.x >> 6; i < 64; i += 4)
-    if (c0 + i < a.cols) reinterpret_cast<uint16_t*>(a.xt)[(c0 + i) * a.pxt + r0 + c] = tile[c][i];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int c = u * 32 + line;
+    if (c0 + c >= a.cols) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = tile[chunk * 8 + 2 * j][c >> 1] >> (c & 1) * 16, hi = tile[chunk * 8 + 2 * j + 1][c >> 1] >> (c & 1) * 16;
+      w[j] = (lo & 0xffff) | hi << 16;
+    }
+    *(uint4*)(a.xt + ((c0 + c) * a.pxt + r0 + chunk * 8) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // --- host ------------------------------------------------------------------------
@@ -550,6 +603,8 @@ int check_newton(const skg_newton_schulz_args_t* a) {
   // Rows of the fp16 operands within 32-bit offsets of a tile of 256.
   constexpr int64_t most = (int64_t(INT32_MAX) / 256) / 2 - 64;
   if (a->rows > most || a->cols > most) return unsupported("dimension too large");
+  // Tiles of every kernel, and the threads of their launches, within 32 bits.
+  if (a->rows && a->cols > (int64_t(1) << 33) / a->rows) return unsupported("rows x cols must be at most 2^33");
   if (a->steps < 1 || a->steps > SKG_NEWTON_SCHULZ_MAX_STEPS) return unsupported("steps must be 1 to SKG_NEWTON_SCHULZ_MAX_STEPS");
   if (a->ldg < a->cols || a->ldo < a->cols) return unsupported("leading dimension too small");
   if (!(a->eps >= 0.f)) return unsupported("eps must not be negative");
@@ -589,15 +644,16 @@ void ns_direct(const NsParams& p, int cus, hipStream_t st) {
 // 88 us on 192 x 192 (253 tiles; 105 on 256 x 256, 136 tiles; 123 on 128 x 128, 528
 // tiles), 4864 x 4096 over 4096 170 on 320 x 256 (256 tiles; 211 on 256 x 256, 304
 // tiles; 197 on 128 x 128).  The direct kernels' waves split K, which a small one
-// needs: fifteen products of 300 x 1111 and the norm take 101 us on 32 x 32, 143 on
-// 64 x 64 and 166 on 128 x 128, those of 1024 x 1024 237, 181 and 222.
+// needs: fifteen products of 300 x 1111 and the norm take 83 us on 32 x 32 (two stages
+// ahead, two workgroups a CU; 97 with four and one), 143 on 64 x 64 and 166 on
+// 128 x 128.
 struct NsKernel {
   int tm, tn, square;  // square: the kernel that takes this one's symmetric products
   double launch, start, stage;
   void (*run)(const NsParams&, int, hipStream_t);
 };
 const NsKernel kNsKernels[SKG_NS_TILE_COUNT] = {
-    /* 32x32   */ {32, 32, 0, 2, 1.2, 0.16, ns_direct<NsDirect<2, 2, 4>>},
+    /* 32x32   */ {32, 32, 0, 2, 1.2, 0.16, ns_direct<NsDirect<2, 2, 2>>},
     /* 64x64   */ {64, 64, 1, 2, 3.3, 0.3, ns_direct<NsDirect<4, 4, 2>>},
     /* 128x128 */ {128, 128, 2, 1, 5, 0.52, ns_ring<NsRing<128, 128, 4>>},
     /* 192x192 */ {192, 192, 3, 1, 12, 0.97, ns_ring<NsRing<192, 192, 3>>},
@@ -657,11 +713,14 @@ int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hip
   in.px = wide ? w.pn : w.pm;
   in.pxt = wide ? w.pm : w.pn;
   in.eps = a->eps;
-  in.blocks = (int)std::min<int64_t>(kSumBlocks, ceil_div(a->rows * ceil_div(a->cols, 8), 256));
+  in.chunks = (uint32_t)(a->rows * ceil_div(a->cols, 8));
+  in.per = make_fastdiv((uint32_t)ceil_div(a->cols, 8));
+  in.across = make_fastdiv((uint32_t)ceil_div(a->cols, 64));
+  in.blocks = (int)std::min<int64_t>(kSumBlocks, ceil_div(in.chunks, 256));
   auto first = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     hipLaunchKernelGGL((ns_sum_kernel<DT>), dim3((unsigned)in.blocks), dim3(256), 0, st, in);
-    hipLaunchKernelGGL((ns_first_kernel<DT>), dim3((unsigned)ceil_div(a->cols, 64), (unsigned)ceil_div(a->rows, 64)), dim3(256), 0, st, in);
+    hipLaunchKernelGGL((ns_first_kernel<DT>), dim3((unsigned)(ceil_div(a->cols, 64) * ceil_div(a->rows, 64))), dim3(256), 0, st, in);
   };
   if (a->dtype == SKG_F16)
     first(std::integral_constant<int, DT_F16>{});

@@ -249,6 +249,7 @@ def update(ws=(0x10000, 1 << 40), **kw):
     (dict(ldg=95), "leading"),
     (dict(ldo=95), "leading"),
     (dict(tile=7), "tile"),
+    (dict(rows=1 << 20, cols=(1 << 13) + 1, ldg=1 << 14, ldo=1 << 14), "2^33"),
     (dict(tile=-2), "tile"),
     (dict(eps=-1.0), "eps"),
     (dict(eps=float("nan")), "eps"),
