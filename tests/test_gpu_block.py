@@ -12,7 +12,10 @@ of the quotient 2^-23 lower and higher.
 Product: a matrix instruction adds 128 products, the blocks are added in fp32;
 with each of the K additions and the blocks' scalings off by at most one unit of
 2^-23 of the sum of magnitudes, (K + 16) 2^-23 of that sum bounds the whole; the
-output's rounding adds half a step."""
+output's rounding adds half a step.  That is all for fp32 outputs.  16-bit ones come
+from 8-bit instructions, which drop what lies 2^-12 under a group's largest product:
+not in that bound, but 1/16 to 1/2 of the half step on top of it, so the tests hold
+16-bit outputs to more than is promised."""
 
 import numpy as np
 import pytest
