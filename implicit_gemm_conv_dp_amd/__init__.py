@@ -28,6 +28,7 @@ position's rotation, and ``newton_schulz`` for the update of its weight.
 
 import contextlib
 import ctypes
+import struct
 
 from . import _lib
 from ._lib import (SkgError, skg_default_pool, skg_device_info, skg_plan_gemm,  # noqa: F401
@@ -86,6 +87,7 @@ _SK_ORDER = _Names(SK_ORDERS, "stream-K order")
 _BLOCK = _Names(BLOCKS, "block shape")
 _STYLE = _Names(ROPE_STYLES, "rotation style")
 _NS_TILE = _Names(NS_TILES, "tile")
+_HEADS = struct.Struct("@2q8i2P6q2P6q4PqPq2P6q2Pf4x")  # skg_heads_args_t
 
 
 def _ptr(t):
@@ -376,21 +378,26 @@ def qknorm_rope_args(q=None, k=None, yq=None, yk=None, dyq=None, dyk=None, *, ba
     dt = _DTYPE[dtype]
     tq, tk = heads_q * head_dim, heads_k * head_dim
     cq, ck = (seq * tq, tq, head_dim), (seq * tk, tk, head_dim)
-    return _lib.skg_heads_args_t(
+    for strides in (q_strides, k_strides, yq_strides, yk_strides, dyq_strides, dyk_strides):
+        if strides is not None and len(strides) != 3:
+            raise ValueError("strides: batch, token and head")
+    # Packed in one call: field by field, strides as structures, it is the longest part
+    # of a small call (13 us; 4 so).
+    return _lib.skg_heads_args_t.from_buffer(bytearray(_HEADS.pack(
         batch, seq, heads_q, heads_k, head_dim, head_dim if rope_dim is None else rope_dim, dt,
         dt if dtype_w is None else _DTYPE[dtype_w], _STYLE[style],
         32 if positions is None else 8 * positions.element_size(),
         0 if q is None else q.data_ptr(), 0 if k is None else k.data_ptr(),
-        q_strides or cq, k_strides or ck,
+        *(cq if q_strides is None else q_strides), *(ck if k_strides is None else k_strides),
         0 if yq is None else yq.data_ptr(), 0 if yk is None else yk.data_ptr(),
-        yq_strides or cq, yk_strides or ck,
+        *(cq if yq_strides is None else yq_strides), *(ck if yk_strides is None else yk_strides),
         0 if weight_q is None else weight_q.data_ptr(),
         0 if weight_k is None else weight_k.data_ptr(),
         0 if cos is None else cos.data_ptr(), 0 if sin is None else sin.data_ptr(), table_rows,
         0 if positions is None else positions.data_ptr(), pos0,
         0 if dyq is None else dyq.data_ptr(), 0 if dyk is None else dyk.data_ptr(),
-        dyq_strides or cq, dyk_strides or ck,
-        0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), eps)
+        *(cq if dyq_strides is None else dyq_strides), *(ck if dyk_strides is None else dyk_strides),
+        0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), eps)))
 
 
 def qknorm_rope(q, k, yq, yk, stream=None, **kw):

@@ -2,7 +2,11 @@
 GPU): every argument check returns -2 with its reason before anything touches
 a device, and empty calls succeed without one."""
 
+import ctypes
+import struct
+
 import pytest
+import torch
 
 import implicit_gemm_conv_dp_amd as skg
 
@@ -278,3 +282,30 @@ def test_empty_update():
     update(cols=0, g=None, out=None, ws=(0, 0))()
     assert skg.skg_newton_schulz_workspace_bytes(skg.newton_schulz_args(rows=0, cols=8, dtype="f32")) == 0
     assert skg.skg_newton_schulz_workspace_bytes(skg.newton_schulz_args(rows=8, cols=8, dtype="f32")) > 0
+
+
+def test_heads_arguments_fill_their_structure():
+    assert skg._HEADS.size == ctypes.sizeof(skg._lib.skg_heads_args_t)
+    t = [torch.empty(4) for _ in range(14)]
+    st = [(10 * i + 1, 10 * i + 2, 10 * i + 3) for i in range(6)]
+    pos = torch.zeros(2, dtype=torch.int64)
+    a = skg.qknorm_rope_args(*t[:6], batch=2, seq=3, heads_q=4, heads_k=5, head_dim=6, rope_dim=2, dtype="bf16",
+                             weight_q=t[6], weight_k=t[7], dtype_w="f32", cos=t[8], sin=t[9], table_rows=11,
+                             positions=pos, pos0=12, style="pairs", eps=0.25, q_strides=st[0], k_strides=st[1],
+                             yq_strides=st[2], yk_strides=st[3], dyq_strides=st[4], dyk_strides=st[5], dwq=t[10],
+                             dwk=t[11])
+    got = {n: getattr(a, n) for n, _ in a._fields_}
+    for n, v in dict(batch=2, seq=3, heads_q=4, heads_k=5, head_dim=6, rope_dim=2, dtype=skg.DTYPES["bf16"],
+                     dtype_w=skg.DTYPES["f32"], style=skg.ROPE_STYLES["pairs"], pos_bits=64, table_rows=11, pos0=12,
+                     eps=0.25, positions=pos.data_ptr()).items():
+        assert got[n] == v, n
+    for n, v in zip(("q", "k", "yq", "yk", "dyq", "dyk", "weight_q", "weight_k", "cos", "sin", "dwq", "dwk"), t):
+        assert got[n] == v.data_ptr(), n
+    for n, v in zip(("q", "k", "yq", "yk", "dyq", "dyk"), st):
+        s = got[n + "_strides"]
+        assert (s.batch, s.token, s.head) == v, n
+    for bad in (dict(seq=2.5), dict(heads_q="4"), dict(q_strides=(1, 2)),
+                dict(q_strides=(1, 2), k_strides=(1, 2, 3, 4)), dict(yq_strides=())):
+        kw = dict(seq=3, heads_q=4, heads_k=5, head_dim=6, dtype="f32")
+        with pytest.raises((TypeError, ValueError, struct.error)):
+            skg.qknorm_rope_args(t[0], t[1], t[2], t[3], **dict(kw, **bad))
