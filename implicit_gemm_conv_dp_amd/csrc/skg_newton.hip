@@ -145,9 +145,9 @@ struct NsDirect {
       for (int k = 0; k < 2; ++k) {
         i32x4 a[FM], b[FN];
 #pragma unroll
-        for (int f = 0; f < FM; ++f) a[f] = *(const SKG_LDS i32x4*)(st + lds_off<RB>(f * 16 + r, k * 4 + q));
+        for (int f = 0; f < FM; ++f) a[f] = *(const SKG_LDS i32x4*)(st + lds_off<RB>(f * 16 + r, 2 * q + k));
 #pragma unroll
-        for (int f = 0; f < FN; ++f) b[f] = *(const SKG_LDS i32x4*)(st + TM * RB + lds_off<RB>(f * 16 + r, k * 4 + q));
+        for (int f = 0; f < FN; ++f) b[f] = *(const SKG_LDS i32x4*)(st + TM * RB + lds_off<RB>(f * 16 + r, 2 * q + k));
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -244,20 +244,22 @@ struct NsRing : Ring8<TM_, TN_, D_, 0> {
   SKG_DEV NsRing(const NsParams& g, SKG_LDS char* l) {
     R::init(l, g.lda_b, g.ldb_b, (g.K + 63) / 64);
     const int r = lane & 15, q = lane >> 4;
-    fra = lds_off<RB>(wm * WTM + r, q);
-    frb = TM * RB + lds_off<RB>(wn * WTN + r, q);
+    fra = lds_off<RB>(wm * WTM + r, 2 * q);
+    frb = TM * RB + lds_off<RB>(wn * WTN + r, 2 * q);
   }
   SKG_DEV void open(const NsParams& g, int m0, int n0) {
     ra = ring_rows(g.A, m0, g.M, g.lda_b, g.lda_b, na);
     rb = ring_rows(g.B, n0, g.N, g.ldb_b, g.ldb_b, nb);
   }
   typedef i32x4 Frag;
-  // A lane's place in a slot at both k-steps: its chunk's number goes up by 4, an XOR
-  // within the permuted row.
+  // A lane's place in a slot at both k-steps: chunks 2q and 2q + 1 of a row, neighbours
+  // in the permuted row.  (Any split of a row's chunks serves, A's and B's alike.  The
+  // LDS serves a 16-byte read to 16 lanes at once, and not those of one q: with chunks q
+  // and 4 + q they met in its banks by twos: 2048 x 2048 346 us, 321 so.)
   struct At {
     const SKG_LDS char* k[2];
   };
-  SKG_DEV At at_k(uint32_t st, uint32_t first) const { return {{lds + (st + first), lds + ((st + first) ^ 64)}}; }
+  SKG_DEV At at_k(uint32_t st, uint32_t first) const { return {{lds + (st + first), lds + ((st + first) ^ 16)}}; }
   template <int ROW>
   SKG_DEV static Frag read_a(const At& p) {
     return *(const SKG_LDS Frag*)(p.k[ROW / FM] + ROW % FM * 16 * RB);
