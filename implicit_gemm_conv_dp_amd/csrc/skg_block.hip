@@ -11,7 +11,9 @@
 //
 // A workgroup takes 128 x 128 elements, from one read for every output that is
 // asked for: the rows' codes go straight from registers, the columns' by way of
-// LDS, so both take whole 128-byte runs.
+// LDS, so both take whole 128-byte runs.  Bound by memory traffic: 16384 x 4096 bf16
+// both ways takes 54 us alone, 60 us one call after another, 4.5 to 5 TB/s of reads
+// and writes (a large copy: 5.4).
 #include <algorithm>
 #include <exception>
 #include <string>

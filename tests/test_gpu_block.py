@@ -269,3 +269,31 @@ def test_repeated_launches_give_the_same_bits():
             multiply(a, sa, b, sb, C, M=M, N=N, K=K, dtype_ab="e4m3", dtype_c="f32", scale_mode="block128", tile=tile)
             first = C if first is None else first
             assert torch.equal(C, first)
+
+
+@pytest.mark.parametrize("tile", DIRECT + RING + ["auto"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype_c", ["bf16", "f32"])
+def test_codes_and_scales_that_are_not_finite(tile, fmt, dtype_c):
+    """NaN and infinite codes and scales, and products past the output's range, reach the
+    rows and columns that they belong to, and no others."""
+    M, N, K = 33, 140, 256
+    a, b = (torch.full((n, K), 0x38 if fmt == "e4m3" else 0x3C, dtype=torch.uint8, device="cuda") for n in (M, N))
+    sa, sb = torch.ones(2, M, device="cuda"), torch.ones(2, N, device="cuda")
+    want = np.full((M, N), float(K))
+    a[3, 200] = 0x7F                       # NaN in both formats
+    want[3] = np.nan
+    if fmt == "e5m2":
+        a[5, 7] = 0xFC                     # -inf
+        b[130, 7] = 0x7C
+        want[5], want[[i for i in range(M) if i not in (3, 5)], 130] = -np.inf, np.inf
+    sa[1, 9] = float("inf")
+    want[9] = np.inf
+    sb[0, 11] = float("nan")
+    want[:, 11] = np.nan
+    sa[0, 12] = 1e38                       # finite, but 128 e38 is not
+    want[12] = np.inf
+    want[12, 11] = want[3, 130] = np.nan
+    c = poison(M, 144, dtype=T[dtype_c])   # rows of whole 16 bytes
+    multiply(a, sa, b, sb, c, M=M, N=N, K=K, ldc=144, dtype_ab=fmt, dtype_c=dtype_c, scale_mode="row128", tile=tile)
+    np.testing.assert_array_equal(f64(c)[:, :N], want)
