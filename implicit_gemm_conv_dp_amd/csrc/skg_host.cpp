@@ -349,6 +349,8 @@ static bool spans_rows(const TileDesc& t, const skg_gemm_args_t* a) {
   return row_bytes(a->dtype_ab, a->lda) <= kMaxBufferBytes / t.tm && row_bytes(a->dtype_ab, a->ldb) <= kMaxBufferBytes / t.tn;
 }
 
+static int resolve_block_tile(const skg_gemm_args_t& r);
+
 // The fp4 tile of a call that leaves it open: the least of the times that these
 // models give, in us, fitted to a sweep of 31 shapes (M 1 to 8192, N 300 to
 // 8192, K 256 to 8192) on all tiles, one call repeated: operands up to 256 MB
@@ -367,8 +369,6 @@ static bool spans_rows(const TileDesc& t, const skg_gemm_args_t* a) {
 //   256x256), 4096x4096x4096 39.9 on 256x256 (45.6 on 256x128, 50.4 on
 //   128x128), 7349x2145x4224 52.2 on 256x128 (56.9 on 128x128, 73.7 on
 //   256x256).
-static int resolve_block_tile(const skg_gemm_args_t& r);
-
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   skg_gemm_args_t r = *a;
   if (block_scales(r.scale_mode)) {
@@ -404,9 +404,8 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
   return r;
 }
 
-// The tile of an 8-bit product with a scale for each 128 of K.
 // The tile of a product with a scale for each 128 of K: the least of the times, in us,
-// that these models give, fitted to 51 shapes from 1 x 4096 x 4096 to 4096 x 4096 x 4096;
+// that these models give, fitted to 46 shapes and types from 1 x 4096 x 4096 to 4096 x 4096 x 4096;
 // the tile they name was within 4 % of the shape's best in all but four, within 15 % in
 // all.  A direct kernel's first round costs `start` and `block` for each 128 of K that
 // one of its four waves takes (the latency of the loads), one more workgroup on each CU
