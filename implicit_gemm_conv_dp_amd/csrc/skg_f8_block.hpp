@@ -83,7 +83,9 @@ SKG_DEV i32x4 f8_scales(const float* s, int64_t lines, int64_t width) {
 // barrier, through LDS of its own, D blocks ahead.  The four partial tiles meet
 // once in LDS and are added in a fixed order: one launch, no workspace.  One row is
 // bound by memory: 1 x 8192 x 8192 11.9 us, 5.6 TB/s of its codes.  Few rows are bound
-// by a tile's chain of loads: 48 x 4863 x 4096 7.9 us, 2.6 TB/s.
+// by a tile's chain of loads: 48 x 4863 x 4096 7.9 us, 2.6 TB/s.  (Eight waves, each
+// with half as many blocks, are slower: 1 x 8192 x 8192 16.2 us against 14.8, both from
+// a graph with operands from memory.)
 template <int FM, int FN, int D, int FMT, bool ROWS, bool EXACT>
 struct F8Direct {
   static constexpr int TM = 16 * FM, TN = 16 * FN, WAVES = 4, RB = 128;
