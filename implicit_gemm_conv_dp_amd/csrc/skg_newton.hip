@@ -13,7 +13,10 @@
 // P 2^11): eleven bits against bf16's eight at the same rate of the matrix
 // instructions, and S of a large matrix, whose entries are around 1/m, stays clear
 // of fp16's subnormals.  Sums, the polynomial and the update are fp32, each
-// rounded once when it is stored; the norm's sum is fp64.
+// rounded once when it is stored; the norm's sum is fp64.  P's diagonal is kept apart
+// in fp32: where X is nearly orthogonal it is near -2.7, and a X + P X what is left of
+// 3.4 X, so its rounding to eleven bits was most of the result's error (64 x 4096
+// 0.0018 of its norm, 0.0008 so; one row 0.0043 and 0.0007).
 //
 // 4864 x 4096 takes 1.58 to 1.68 ms, five steps of three products at 0.87 to 0.96
 // PFLOP/s (S 88 us, P 79, Y 170), the norm and first forms 65 us.  The matrix units are
@@ -50,6 +53,11 @@ struct NsParams {
   uint32_t lda_b, ldb_b;     // bytes
   int64_t ldd, ldc, ldct;    // elements
   float alpha, beta;
+  // The diagonal of a symmetric product apart from it: ctn floats, and zeros in C.  And
+  // of B: C = alpha A (B + diag) + beta D where D is A, so D's column n counts
+  // beta + alpha diag[n] times.
+  float* diag_out;
+  const float* diag_in;
   int dt;                    // of C and Ct: DT_F16, DT_BF16 or DT_F32
   int vec;                   // C and Ct are aligned to 16 bytes
   int sym;                   // M == N: tiles on and below the diagonal; Ct is C
@@ -134,11 +142,16 @@ struct NsDirect {
       return f < FM * FN;
     };
     uint2 d[PART];
+    f32x4 more[PART];
 #pragma unroll
     for (int k = 0; k < PART; ++k) {
       int m, n;
       d[k] = make_uint2(0, 0);
-      if (place(k, m, n) && g.D && m < g.M && n < g.cn) d[k] = *(const uint2*)(g.D + ((int64_t)m * g.ldd + n) * 2);
+      more[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (place(k, m, n) && g.D && m < g.M && n < g.cn) {
+        d[k] = *(const uint2*)(g.D + ((int64_t)m * g.ldd + n) * 2);
+        if (g.diag_in) more[k] = *(const f32x4*)(g.diag_in + n);
+      }
     }
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -194,7 +207,17 @@ struct NsDirect {
       const i32x4 w = {(int)d[k].x, (int)d[k].y, 0, 0};
       float x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(v[e], g.alpha, half_at(w, e) * g.beta);
+      for (int e = 0; e < 4; ++e)
+        x[e] = __builtin_fmaf(v[e], g.alpha, half_at(w, e) * __builtin_fmaf(g.alpha, more[k][e], g.beta));
+      if (g.diag_out) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (m == n + e) {
+            if (m < g.ctn) g.diag_out[m] = x[e];
+            x[e] = 0.f;
+          }
+        }
+      }
       auto put = [&](char* base, int64_t at, float y) {
         if (g.dt == DT_F32)
           ((float*)base)[at] = y;
@@ -324,7 +347,7 @@ struct NsRing : Ring8<TM_, TN_, D_, 0> {
       static_for<0, PER>([&](auto n_) { R::template dma_rows<decltype(n_)::value>(j, dst(j)); });
     });
   }
-  // acc = D beta / alpha, so that alpha acc is alpha A B^T + beta D at the end: D's
+  // acc = D (beta / alpha + diag), so that alpha acc is all of C at the end: D's
   // loads travel with the first stages; behind a tile's stores they were waited for
   // (40 us of a 4096 x 4096 product).  (D's rows are whole 128 bytes: columns come in
   // fours.)
@@ -332,6 +355,13 @@ struct NsRing : Ring8<TM_, TN_, D_, 0> {
     const float ratio = g.beta / g.alpha;
     const __amdgpu_buffer_rsrc_t rd =
         make_rsrc_uniform(g.D + (int64_t)m0 * g.ldd * 2, (uint32_t)min((int64_t)max(g.M - m0, 0) * g.ldd * 2, (int64_t)0x7fffffff));
+    f32x4 by[FN];
+#pragma unroll
+    for (int n = 0; n < FN; ++n) {
+      const int c = n0 + wn * WTN + n * 16 + 4 * (lane >> 4);
+      by[n] = f32x4{ratio, ratio, ratio, ratio};
+      if (g.diag_in && c < g.cn) by[n] += *(const f32x4*)(g.diag_in + c);
+    }
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       i32x2 d[FN];
@@ -344,7 +374,7 @@ struct NsRing : Ring8<TM_, TN_, D_, 0> {
 #pragma unroll
       for (int n = 0; n < FN; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][n][e] = half_at(i32x4{d[n][0], d[n][1], 0, 0}, e) * ratio;
+        for (int e = 0; e < 4; ++e) acc[f][n][e] = half_at(i32x4{d[n][0], d[n][1], 0, 0}, e) * by[n][e];
     }
   }
   SKG_DEV void zero() {
@@ -382,8 +412,17 @@ struct NsRing : Ring8<TM_, TN_, D_, 0> {
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n = 0; n < FN; ++n) {
-          const f32x4 v = acc[2 * h + k][n] * g.alpha;
+          f32x4 v = acc[2 * h + k][n] * g.alpha;
           const int row = k * 16 + r;
+          if (diagonal && g.diag_out) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (m + row == c0 + n * 16 + 4 * q + e) {
+                if (m + row < g.ctn) g.diag_out[m + row] = v[e];
+                v[e] = 0.f;
+              }
+            }
+          }
           if constexpr (DT == DT_F32) {
             if (g.C) {
               *(SKG_LDS f32x4*)(st + strip_off<4, WTN>(row, n * 4 + q)) = v;
@@ -577,10 +616,10 @@ bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 int64_t pitch_of(int64_t n) { return ceil_div(n, 64) * 64; }
 
 // The workspace: partial sums, X and Y twice (a step reads one pair and writes the
-// other), S and P.
+// other), S, P and P's diagonal.
 struct NsSpace {
   int64_t m, n, pm, pn;
-  size_t x[2], y[2], s, p, bytes;
+  size_t x[2], y[2], s, p, diag, bytes;
 };
 NsSpace ns_space(const skg_newton_schulz_args_t* a) {
   NsSpace w;
@@ -600,6 +639,7 @@ NsSpace ns_space(const skg_newton_schulz_args_t* a) {
   }
   w.s = take(w.m, w.pm);
   w.p = take(w.m, w.pm);
+  w.diag = take(2, w.pm);  // P's diagonal, fp32
   w.bytes = at;
   return w;
 }
@@ -763,11 +803,14 @@ int run_newton(const skg_newton_schulz_args_t* a, void* ws, size_t ws_bytes, hip
     p.C = p.Ct = poly;
     p.alpha = cc * (kScaleP / (kScaleS * kScaleS));
     p.beta = cb * (kScaleP / kScaleS);
+    p.diag_out = reinterpret_cast<float*>(base + w.diag);
     if (e == hipSuccess) e = ns_product(p, a->tile, cus, st);
     // Y <- a Y + Y P, and X
     const bool last = i + 1 == a->steps;
     p.A = p.D = y;
     p.B = poly;
+    p.diag_out = nullptr;
+    p.diag_in = reinterpret_cast<const float*>(base + w.diag);
     p.M = n;
     p.N = m;
     p.sym = 0;

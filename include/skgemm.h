@@ -729,9 +729,10 @@ int skg_plan_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t 
  * (S = X^T X on the other side where G has more rows than columns, which is the
  * same).  coefficients holds a, b, c of each step (3 x steps host floats).  The
  * norm is summed in fp64.  Between the products X and S are kept in fp16 with a
- * fixed power of two each (2^13 and 2^12, the polynomial 2^11): ten or more
+ * fixed power of two each (2^13 and 2^12, the polynomial 2^11, its diagonal
+ * apart in fp32): ten or more
  * binades below the largest entry keep their eleven bits, and entries of X up to
- * 7, of S up to 15 and of b S + c S^2 up to 31 fit; coefficients that drive them
+ * 7, of S up to 15 and of b S + c S^2 beside its diagonal up to 31 fit; coefficients that drive them
  * further give infinities or NaN.  Sums are fp32.  dtype_out is SKG_BF16,
  * SKG_F16 or SKG_F32 (the last is not rounded, but is no more exact than the
  * fp16 factors make it).  G is read before out is written, so out may be G where

@@ -94,7 +94,8 @@ def head_norm_bwd(dy, x, w, eps, cos, sin, style):
 
 def newton_schulz(g, coefficients, eps, scale=1.0, rounded=False):
     """``coefficients``: rows of (a, b, c).  ``rounded``: X, S and the polynomial
-    kept as fp16 times 2^13, 2^12 and 2^11, as the GPU keeps them."""
+    kept as fp16 times 2^13, 2^12 and 2^11, the polynomial's diagonal apart and
+    unrounded, as the GPU keeps them."""
     def keep(v, power):
         if not rounded:
             return v
@@ -106,7 +107,9 @@ def newton_schulz(g, coefficients, eps, scale=1.0, rounded=False):
     x = keep(x / (np.sqrt(np.sum(x * x)) + eps), 13)
     for i, (a, b, c) in enumerate(coefficients):
         s = keep(x @ x.T, 12)
-        p = keep(b * s + c * (s @ s), 11)
+        p = b * s + c * (s @ s)
+        d = np.diag(np.diag(p))
+        p = keep(p - d, 11) + d
         x = a * x + p @ x
         if i + 1 < len(coefficients):
             x = keep(x, 13)

@@ -54,7 +54,7 @@ def check(got, g, dtype_out, coefficients=(MUON,) * 5, eps=EPS, scale=1.0):
     assert off <= 1.5 * own + (2.0 ** -14 + HALF[dtype_out]) * n, (off / n, own / n)
 
 
-SHAPES = [(1, 1), (1, 300), (300, 1), (5, 3), (33, 70), (64, 64), (70, 33), (128, 200), (200, 129), (300, 1111), (257, 256)]
+SHAPES = [(1, 1), (1, 300), (300, 1), (5, 3), (33, 70), (64, 64), (70, 33), (128, 200), (200, 129), (300, 1111), (257, 256), (64, 4096)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
