@@ -18,11 +18,11 @@
 // 3.4 X, so its rounding to eleven bits was most of the result's error (64 x 4096
 // 0.0018 of its norm, 0.0008 so; one row 0.0043 and 0.0007).
 //
-// 4864 x 4096 takes 1.58 to 1.68 ms, five steps of three products at 0.87 to 0.96
+// 4864 x 4096 takes 1.63 to 1.66 ms, five steps of three products at 0.87 to 0.96
 // PFLOP/s (S 88 us, P 79, Y 170), the norm and first forms 65 us.  The matrix units are
 // busy 48 % of the time: a product is one round of tiles, so a seventh of it is filling
 // the ring and writing both forms with nothing behind it (40 MB each, at once), and
-// the main loop waits for its loads.  300 x 1111 takes 82 us, seventeen launches of
+// the main loop waits for its loads.  300 x 1111 takes 84 us, seventeen launches of
 // 3.5 to 6 us.
 //
 // Rows in the workspace are padded to whole 128 bytes with zeros: a product of
