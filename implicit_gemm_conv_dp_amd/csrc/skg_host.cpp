@@ -410,8 +410,8 @@ skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a) {
 // all.  A direct kernel's first round costs `start` and `block` for each 128 of K that
 // one of its four waves takes (the latency of the loads), one more workgroup on each CU
 // `more` and `each` (their rate).  A ring kernel's round costs `more` and `each` a stage.
-// An fp32 output's stages cost nearly twice (its matrix instructions are fp16's), and
-// 256 x 256 has no registers for them; a scale a column costs another 8 to 15 %.
+// An fp16 or fp32 output's stages cost nearly twice (their matrix instructions are fp16's),
+// and 256 x 256 has no registers for them; a scale a column costs another 8 to 15 %.
 //
 //                       16x16   16x32   32x32   32x64   64x64   128x128  256x128  256x256
 //   1 x 4096 x 4096       5.8     6.5     7.4     9.8    12.8     19.2     27.8     47.0
@@ -431,7 +431,7 @@ static int resolve_block_tile(const skg_gemm_args_t& r) {
   };
   int best_tile = SKG_TILE_64x64x128;  // also for sizes that are refused
   if (r.M <= 0 || r.N <= 0 || r.K <= 0) return best_tile;
-  const bool exact = r.dtype_c == SKG_F32;
+  const bool exact = r.dtype_c != SKG_BF16;
   double best = 1e300;
   for (const auto& m : kModels) {
     const TileDesc& t = kTiles[m.tile];

@@ -107,10 +107,15 @@ enum skg_scale_mode {
    * lines of ceil(N/128), as a weight's are).  These are the arrays that
    * skg_run_block_quant writes.  Each array is at most 2^31 - 1 bytes.  Tiles:
    * SKG_TILE_AUTO, 256x256x128, 128x128x128 and those of this mode alone; mode
-   * dp or auto (which is dp), no workspace.  f32 outputs hold fp32 sums of exact
-   * products; f16 and bf16 ones come from the 8-bit matrix instructions, which
-   * drop what lies some 2^-12 under the largest product of a block (sums of
-   * normal data are 1.3e-5 off before they are rounded). */
+   * dp or auto (which is dp), no workspace.  f32 and f16 outputs hold fp32 sums of
+   * exact products.  bf16 ones come from the 8-bit matrix instructions, which
+   * cut each product, towards zero, at 2^-13 of the largest one of its eight
+   * consecutive K (for this the largest exponents count, a subnormal code's as
+   * the smallest normal one's).  A group's sum is so off by at most 7 2^-13 of
+   * that product, all of C before its rounding by less than 2^-10 of the sum of
+   * magnitudes where the largest products are of normal codes; sums of normal
+   * data by 1.3e-5.  That is below a bf16 rounding unless the sum cancels:
+   * where it does, an f32 output is to be asked for. */
   SKG_SCALE_BLOCK128 = 3,
   SKG_SCALE_ROW128 = 4
 };
