@@ -105,7 +105,10 @@ enum skg_scale_mode {
    * alike (both operands quantised along K, as a weight gradient's are); with
    * SKG_SCALE_BLOCK128 one float stands for 128 consecutive columns too (K/128
    * lines of ceil(N/128), as a weight's are).  These are the arrays that
-   * skg_run_block_quant writes.  Each array is at most 2^31 - 1 bytes.  Tiles:
+   * skg_run_block_quant writes.  sa sb is taken first, in fp32: where it is not
+   * within 2^-126 and fp32's largest number, a block that is not all zeros loses
+   * bits or is 0, infinite or NaN, although its term may be a number that fp32
+   * holds.  Each array is at most 2^31 - 1 bytes.  Tiles:
    * SKG_TILE_AUTO, 256x256x128, 128x128x128 and those of this mode alone; mode
    * dp or auto (which is dp), no workspace.  f32 and f16 outputs hold fp32 sums of
    * exact products.  bf16 ones come from the 8-bit matrix instructions, which
