@@ -657,7 +657,9 @@ int check_newton(const skg_newton_schulz_args_t* a) {
   if (a->ldg < a->cols || a->ldo < a->cols) return unsupported("leading dimension too small");
   if (!(a->eps >= 0.f)) return unsupported("eps must not be negative");
   if (a->tile < SKG_NS_TILE_AUTO || a->tile >= SKG_NS_TILE_COUNT) return unsupported("unknown tile");
-  if (!std::isfinite(a->scale)) return unsupported("scale must be finite");
+  // The last step's factors are scale times 2^-24 and less: normal numbers of fp32.
+  if (!std::isfinite(a->scale) || (a->scale != 0.f && std::fabs(a->scale) < 0x1p-100f))
+    return unsupported("scale must be finite, and 0 or at least 2^-100 in magnitude");
   return SKG_OK;
 }
 

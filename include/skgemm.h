@@ -745,7 +745,8 @@ int skg_plan_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t 
  * SKG_F16 or SKG_F32 (the last is not rounded, but is no more exact than the
  * fp16 factors make it).  G is read before out is written, so out may be G where
  * their types and pitches agree.  A matrix without elements writes nothing.  rows
- * and cols are at most 2^22 - 65, rows x cols 2^33. */
+ * and cols are at most 2^22 - 65, rows x cols 2^33; scale is finite, and 0 or at
+ * least 2^-100 in magnitude. */
 #define SKG_NEWTON_SCHULZ_MAX_STEPS 64
 /* The products' tiles.  AUTO picks each product's from its sizes; otherwise all take
  * this one, but a symmetric product the square one of its width, and a step with
