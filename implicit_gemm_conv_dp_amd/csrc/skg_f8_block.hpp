@@ -262,11 +262,12 @@ struct F8Direct {
 // --- many tiles ------------------------------------------------------------------
 // 8192 x 8192 x 8192 to bf16 takes 440 to 460 us, 2.4 to 2.5 PFLOP/s; its matrix
 // units are busy 63 % of the time at a clock that power brings down to 1.9 GHz.  To
-// fp32 4096 x 4864 x 8192 takes 305 us (a scale a column: 335), 1.07 PFLOP/s: bound by
-// the vector unit, which converts two operands' codes for every product of fragments
-// (two waves' conversions, scalings and products of a 16 x 16 x 128 piece take it some
-// 180 cycles, the matrix unit 128).  Converting them at the end of a stage, with the
-// matrix unit idle, it took 361.
+// fp32 4096 x 4864 x 8192 takes 305 us (a scale a column: 335), 1.07 PFLOP/s: 608 tiles,
+// two full rounds and one of 96.  A stage of two waves then takes 1.6 to 1.75 us.  Its
+// conversions of both operands' codes for every product of fragments, its scalings and
+// its products take the vector unit 1.07 of them and the matrix unit 0.93, each by
+// itself; how much of the rest is the two not overlapping has not been measured.
+// Converting the codes at the end of a stage, with the matrix unit idle, it took 361.
 //
 // Eight waves on a ring of D stages, a stage a block of 128 of K; a wave's part of
 // the tile in 16 x 16 pieces.  Per stage a wave holds its columns' fragments and

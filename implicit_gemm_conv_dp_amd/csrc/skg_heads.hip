@@ -86,7 +86,7 @@ SKG_DEV void load_floats(float (&v)[N], const float* p) {
 
 // What element e0 + j of a token's heads is turned by: y = n c + m s, m the
 // other element of its pair; c = 1 and s = 0 past the rotated ones.  A position
-// outside the table reads nothing and gives NaN.
+// outside the table reads row 0 in its place and gives NaN.
 struct Turn {
   float c[8], s[8];
 };
@@ -374,12 +374,14 @@ bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 
 int lanes_of(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
-// Heads of one token that a group takes: most of them where that leaves enough
-// groups to fill the device.
+// Heads of one token that a group takes, of queries and of keys alike: `most` where
+// that leaves enough groups to fill the device.  (A set of fewer heads than that takes
+// its last one again, and drops the result.)
 int heads_a_group(int64_t tokens, int heads, int lanes, int most) {
   return tokens * ceil_div(heads, most) * lanes >= int64_t(64) * 4096 ? most : 1;
 }
-// Shares of queries or keys: heads in fours (or one by one) for each token.
+// Shares of queries or keys: heads in fours (the gradient: twos) or one by one for
+// each token.
 int64_t shares(int64_t tokens, int heads, int u) { return tokens * ceil_div(heads, u); }
 
 struct HeadPlan {

@@ -77,7 +77,8 @@ int resolve_sk_order(int requested, bool wgrad);
 
 // Argument checks that need no device (a0 of the hot path).
 int validate_gemm(const skg_gemm_args_t* a);
-// *a with SKG_TILE_AUTO resolved (fp4 only; other arguments unchanged).
+// *a with SKG_TILE_AUTO resolved (fp4, and fp8 with a scale for each 128 of K; other
+// arguments unchanged).
 skg_gemm_args_t resolve_gemm(const skg_gemm_args_t* a);
 int validate_wgrad(const skg_wgrad_args_t* a);
 int validate_conv(const skg_conv_args_t* a, bool dgrad);

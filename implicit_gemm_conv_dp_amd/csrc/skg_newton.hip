@@ -18,12 +18,14 @@
 // 3.4 X, so its rounding to eleven bits was most of the result's error (64 x 4096
 // 0.0018 of its norm, 0.0008 so; one row 0.0043 and 0.0007).
 //
-// 4864 x 4096 takes 1.63 to 1.66 ms, five steps of three products at 0.87 to 0.96
+// 4864 x 4096 takes 1.63 to 1.69 ms, five steps of three products at 0.87 to 0.96
 // PFLOP/s (S 88 us, P 79, Y 170), the norm and first forms 65 us.  The matrix units are
 // busy 48 % of the time: a product is one round of tiles, so a seventh of it is filling
 // the ring and writing both forms with nothing behind it (40 MB each, at once), and
 // the main loop waits for its loads.  300 x 1111 takes 84 us, seventeen launches of
-// 3.5 to 6 us.
+// 3.5 to 6 us.  Where X is flat, S has few tiles over a long K, which nothing splits
+// further than a workgroup's four waves: 64 x 4096 (three tiles of 32 x 32) takes 84 us,
+// 256 x 16384 212, and 2048 x 2048 (136 tiles of 128 x 128 on 256 CUs) 348.
 //
 // Rows in the workspace are padded to whole 128 bytes with zeros: a product of
 // padded operands is zero there, so the copy-out keeps the padding zero by writing
@@ -689,7 +691,12 @@ void ns_direct(const NsParams& p, int cus, hipStream_t st) {
 }
 
 // The kernel and tile of a product: the least of the times that these models give, in
-// us, rounds x (start + stages x stage) of a workgroup a CU and the launch.  What counts
+// us, rounds x (start + stages x stage) of a workgroup a CU and the launch.  They are
+// rough: set by the sizes named here on the first forms of the ring kernels, some 10 %
+// over what 256 x 256 and 128 x 128 take now, and for one workgroup of 32 x 32 a CU
+// where two fit.  But on thirteen sizes from 64 x 4096 to 5120 x 5120 the update they
+// choose took at most 7 % longer than the best with one tile for all its products
+// (2048 x 2048 348 us, 325 on 128 x 128), and up to 28 % less.  What counts
 // most for a large one is how full the last round is: 4096 x 4096 symmetric over 4864
 // 88 us on 192 x 192 (253 tiles; 105 on 256 x 256, 136 tiles; 123 on 128 x 128, 528
 // tiles), 4864 x 4096 over 4096 170 on 320 x 256 (256 tiles; 211 on 256 x 256, 304

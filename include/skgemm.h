@@ -236,7 +236,8 @@ enum skg_tile {
   SKG_TILE_256x256x64 = 1,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x256x128 = 2,  /* fp8 GEMM (also with MX block scales), 4 waves;
                                 with a scale for each 128 of K, 8
-                                waves (the plan says so) */
+                                waves (the plan says so), and to f16 and
+                                f32 slower than 256x128x128: too few registers */
   SKG_TILE_32x64x64 = 3,     /* f16/bf16 wgrad (small per-group M), 4 waves */
   SKG_TILE_128x128x64 = 4,   /* f16/bf16 GEMM and wgrad, 4 waves */
   SKG_TILE_256x128x64 = 5,   /* f16/bf16 GEMM and wgrad, 4 waves */
@@ -687,7 +688,7 @@ int skg_run_block_quant(const skg_block_quant_args_t* args, void* stream);
  * Everything is fp32 up to y's rounding.  positions holds batch x seq whole
  * numbers of pos_bits bits, or is NULL: token t of each batch is at pos0 + t.  A
  * position outside the table's table_rows rows gives NaN in the turned elements
- * and reads nothing.
+ * and reads nothing outside the table.
  *
  * The gradient: with g = dy turned back,
  *   dx = s (g weight - x s^2 mean(g weight x));   dw = sum of g x s over tokens
@@ -738,10 +739,13 @@ int skg_plan_run_qknorm_rope_bwd(const skg_heads_args_t* args, void* ws, size_t 
  * same).  coefficients holds a, b, c of each step (3 x steps host floats).  The
  * norm is summed in fp64.  Between the products X and S are kept in fp16 with a
  * fixed power of two each (2^13 and 2^12, the polynomial 2^11, its diagonal
- * apart in fp32): ten or more
- * binades below the largest entry keep their eleven bits, and entries of X up to
- * 7, of S up to 15 and of b S + c S^2 beside its diagonal up to 31 fit; coefficients that drive them
- * further give infinities or NaN.  Sums are fp32.  dtype_out is SKG_BF16,
+ * apart in fp32), whatever the types of G and out: entries of X from 2^-27, of S
+ * from 2^-26 and of b S + c S^2 beside its diagonal from 2^-25 on keep eleven bits,
+ * smaller ones are whole multiples of 2^-37, 2^-36 and 2^-35 (so X loses bits, and
+ * in the end all, where |G| is millions of times below eps).  Entries of X up to
+ * 7, of S up to 15 and of the polynomial up to 31 fit; coefficients that drive
+ * them further give infinities or NaN.  Five steps of the coefficients 3.4445,
+ * -4.775, 2.0315 come out some 0.0008 of their norm off.  Sums are fp32.  dtype_out is SKG_BF16,
  * SKG_F16 or SKG_F32 (the last is not rounded, but is no more exact than the
  * fp16 factors make it).  G is read before out is written, so out may be G where
  * their types and pitches agree.  A matrix without elements writes nothing.  rows
