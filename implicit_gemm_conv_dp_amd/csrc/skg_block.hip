@@ -78,7 +78,7 @@ SKG_DEV float quotient(float v, const Quotient& r) {
 // rounding of that to fewer bits is the real quotient's.
 SKG_DEV float quotient_odd(float v, const Quotient& r) {
   const float n = v * r.a, lost = __builtin_fmaf(v, r.a, -n), q = n * r.inv;
-  const float near = __builtin_fmaf(lost - __builtin_fmaf(q, r.t, -n), r.inv, q);
+  const float near = __builtin_fmaf(-(__builtin_fmaf(q, r.t, -n) - lost), r.inv, q);
   const float left = __builtin_fmaf(-near, r.t, n) + lost;  // its sign is exact
   const uint32_t b = __builtin_bit_cast(uint32_t, near), below = (__builtin_bit_cast(uint32_t, left) ^ b) >> 31;
   return __builtin_islessgreater(left, 0.f) && near != 0.f ? from_bits((b - below) | 1) : near;

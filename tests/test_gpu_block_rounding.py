@@ -19,7 +19,7 @@ from test_gpu_block import poison
 pytestmark = pytest.mark.gpu
 
 
-def near_borders(seed, rows, cols, fmt, block, power):
+def near_borders(seed, rows, cols, fmt, block, power, zeros=0.0):
     rng = np.random.default_rng(seed)
     v = codecs.decode(fmt, np.arange(128))
     v = np.sort(v[np.isfinite(v)])
@@ -31,6 +31,8 @@ def near_borders(seed, rows, cols, fmt, block, power):
     x = (x.view(np.int32) + rng.integers(-1, 2, x.shape, dtype=np.int32)).view(np.float32)
     x = np.minimum(x, wide.astype(np.float32)) * rng.choice([-1, 1], x.shape).astype(np.float32)
     x[::h, ::128] = wide[::h, ::128]
+    x[rng.random(x.shape) < zeros] = 0.0
+    x[rng.random(x.shape) < zeros] = -0.0
     return x
 
 
@@ -60,3 +62,18 @@ def test_elements_next_to_a_border(fmt, block, along, power):
             ws, wq = pj.block_quantize(m.astype(np.float64), fmt, block)
             assert np.array_equal(scales.cpu().numpy(), ws)
             assert np.array_equal(got.cpu().numpy(), wq), (got.cpu().numpy() != wq).sum()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block", ["1x128", "128x128"])
+def test_zeros_next_to_such_elements(fmt, block):
+    """Zeros of both signs and quotients far below the smallest code keep their signs."""
+    x = near_borders(7, 130, 256, fmt, block, 0, zeros=0.2)
+    x[5, 1:] *= np.float32(2.0 ** -60)
+    q, qt = poison(130, 256), poison(256, 256)
+    tall = block == "128x128"
+    s, st = poison(2, 2 if tall else 130, dtype=torch.float32), poison(2, 2 if tall else 256, dtype=torch.float32)
+    skg.block_quant(torch.from_numpy(x).cuda(), q, s, qt, st, rows=130, cols=256, dtype="f32", dtype_q=fmt, block=block)
+    torch.cuda.synchronize()
+    for m, got in ((x, q), (x.T, qt)):
+        assert np.array_equal(got.cpu().numpy()[:, :m.shape[1]], pj.block_quantize(m.astype(np.float64), fmt, block)[1][:, :m.shape[1]])
