@@ -9,7 +9,7 @@
 // rounded to a code: a reciprocal and one residual step, four operations an
 // element.  One that is not just between two codes is 2^-16 of itself away from
 // there, so its rounding to fp32 stays on its side.  fp32 inputs' quotients can be
-// closer than that: those that come near a border are rounded to odd instead.
+// closer than that: of those that come near a border the side is decided exactly.
 //
 // A workgroup takes 128 x 128 elements, from one read for every output that is
 // asked for: the rows' codes go straight from registers, the columns' by way of
@@ -73,15 +73,17 @@ SKG_DEV float quotient(float v, const Quotient& r) {
   const float over = __builtin_fmaf(q, r.t, -n);  // (this way round a -0 stays one)
   return __builtin_fmaf(-over, r.inv, q);
 }
-// The same for an fp32 element, whose product with a is not exact, rounded to odd: the
-// fp32 below the real quotient, with its last bit set where anything is left.  A
-// rounding of that to fewer bits is the real quotient's.
-SKG_DEV float quotient_odd(float v, const Quotient& r) {
-  const float n = v * r.a, lost = __builtin_fmaf(v, r.a, -n), q = n * r.inv;
-  const float near = __builtin_fmaf(-(__builtin_fmaf(q, r.t, -n) - lost), r.inv, q);
-  const float left = __builtin_fmaf(-near, r.t, n) + lost;  // its sign is exact
-  const uint32_t b = __builtin_bit_cast(uint32_t, near), below = (__builtin_bit_cast(uint32_t, left) ^ b) >> 31;
-  return __builtin_islessgreater(left, 0.f) && near != 0.f ? from_bits((b - below) | 1) : near;
+// The same for an fp32 element, whose product with a is not exact, from a quotient q at
+// most three steps of fp32 off: a number on the real quotient's side of every border
+// between codes, or on the border.  Borders have few bits, so none but q rounded to a
+// multiple of eight steps can lie between the two; what v a exceeds that times t by is
+// exact but for the last addition, which keeps its sign.
+SKG_DEV float quotient_side(float v, float q, const Quotient& r) {
+  const uint32_t b = (__builtin_bit_cast(uint32_t, q) + 4) & ~7u;
+  const float n = v * r.a, lost = __builtin_fmaf(v, r.a, -n);
+  const float left = __builtin_fmaf(-from_bits(b), r.t, n) + lost;
+  const int side = (int)(__builtin_bit_cast(uint32_t, left) ^ b) >> 31 | 1;  // away from zero or towards it
+  return from_bits(b + (left == 0.f ? 0 : side));
 }
 template <bool E5M2>
 SKG_DEV uint2 pack_codes(const float (&v)[8]) {
@@ -129,10 +131,11 @@ SKG_DEV uint2 block_codes(const Chunk<DT>& c, const Quotient& r) {
     // A product with the rounded a / t is at most three steps of fp32 off.  That is
     // enough unless it is within four of a border: just between two normal codes, where
     // the bit after a code's last one is set and no later one, or between subnormal
-    // ones, below the smallest normal one (zeros aside).  Then all eight are
-    // divided; of normal data it is one wave in 30, so this is also the faster way:
-    // 16384 x 4096 to e4m3 both ways takes 86 us, 96 with a residual step for each element
-    // and 107 with every one rounded to odd.
+    // ones, below the smallest normal one (zeros aside).  Then the sides of all eight
+    // are decided.  Of normal data it is one wave in 30: 16384 x 4096 to e4m3 both ways
+    // takes 86 us (88 with a residual step for each element, which is not enough; 107
+    // with an exact remainder for each).  Of bf16 values held in fp32, whose quotients
+    // often are borders, it is most: 95 us (83), and 512 x 1152 to e5m2 8.0 (6.7).
     constexpr int HALF = E5M2 ? 20 : 19;
     constexpr uint32_t NORMAL = (E5M2 ? 127u - 14u : 127u - 6u) << 24;
     const float rate = r.a * r.inv;
@@ -144,9 +147,9 @@ SKG_DEV uint2 block_codes(const Chunk<DT>& c, const Quotient& r) {
       border = min(border, (b + (1u << HALF) + 4) << (31 - HALF));
       small = min(small, (b << 1) - 1);  // (zeros wrap around)
     }
-    if (__builtin_expect(border <= 8u << (31 - HALF) || small < NORMAL - 1, 0)) {
+    if (border <= 8u << (31 - HALF) || small < NORMAL - 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = quotient_odd(c.get(j), r);
+      for (int j = 0; j < 8; ++j) v[j] = quotient_side(c.get(j), v[j], r);
     }
   }
   return pack_codes<E5M2>(v);
